@@ -37,7 +37,8 @@ C_SYMBOLS = ("mla_row_width", "mla_status_string", "mla_cache_append", "mla_abso
              "mla_get_device_status", "mla_decode_attn_noalloc", "mla_selftest_wait_timeout",
              "mla_kv_shared_decode_dims", "mla_kv_shared_query", "mla_kv_shared_output",
              "mla_down_kv_append", "mla_out_proj_workspace_size",
-             "mla_out_proj", "mla_decode_step")
+             "mla_out_proj", "mla_decode_step", "mla_q8_page_bytes", "mla_cache_append_q8",
+             "mla_cache_read_q8", "mla_decode_attn_q8")
 
 
 class MlaError(RuntimeError):
@@ -118,6 +119,15 @@ def lib() -> ctypes.CDLL:
                                   _P, _P, _I64, _P, _I32, _P, _I32, _I32, _I32, _I32, _I32, _P,
                                   _P, ctypes.c_size_t, _P, _P, _P, _P]
     L.mla_decode_step.restype = _I32
+    L.mla_q8_page_bytes.argtypes = [D]
+    L.mla_q8_page_bytes.restype = _I64
+    L.mla_cache_append_q8.argtypes = [D, _P, _P, _P, _P, _P, _I32, _P, _P, _I32, _I32, _P, _I64,
+                                      _P, _P]
+    L.mla_cache_append_q8.restype = _I32
+    L.mla_cache_read_q8.argtypes = [D, _P, _I64, _P, _I32, _P, _P, _I32, _I32, _P, _P, _P]
+    L.mla_cache_read_q8.restype = _I32
+    L.mla_decode_attn_q8.argtypes = L.mla_decode_attn.argtypes
+    L.mla_decode_attn_q8.restype = _I32
     _lib = L
     return L
 
@@ -132,6 +142,23 @@ def _stream(stream) -> ctypes.c_void_p:
     if isinstance(stream, torch.cuda.Stream):
         return ctypes.c_void_p(stream.cuda_stream)
     return ctypes.c_void_p(int(stream))
+
+
+def _one_device(tensors, stream):
+    """Context of a call on the device that holds all of `tensors` (and `stream`, if it is a
+    torch stream), so that the launch goes to that device and to its current stream."""
+    dev = None
+    for t in tensors:
+        if t is None:
+            continue
+        if dev is None:
+            dev = t.device
+        elif t.device != dev:
+            raise MlaError(f"tensors are on {dev} and on {t.device}", MLA_ERR_INVALID_ARG)
+    if isinstance(stream, torch.cuda.Stream) and stream.device != dev:
+        raise MlaError(f"the stream is on {stream.device}, the tensors are on {dev}",
+                       MLA_ERR_INVALID_ARG)
+    return torch.cuda.device(dev)
 
 
 def _check(status: int, what: str) -> None:
@@ -319,6 +346,101 @@ def mla_out_up(dims: MlaDims, o_latent, w_uv, o, bias=None,
     _check(st, "mla_out_up")
 
 
+def mla_q8_page_bytes(dims: MlaDims) -> int:
+    """Bytes of a page of the 8-bit cache, or -1 if these dims cannot have one."""
+    return int(lib().mla_q8_page_bytes(ctypes.byref(dims)))
+
+
+def _need_q8(dims: MlaDims, cache, block_table, B: int) -> None:
+    _need(cache, "cache", torch.uint8)
+    want = mla_q8_page_bytes(dims)
+    if want < 0:
+        raise MlaError("dims cannot have an 8-bit cache", MLA_ERR_UNSUPPORTED)
+    if cache.dim() != 2 or cache.shape[1] != want:
+        raise MlaError(f"cache must be [num_pages, {want}], got {tuple(cache.shape)}",
+                       MLA_ERR_INVALID_ARG)
+    _need(block_table, "block_table", torch.int32)
+    if block_table.dim() != 2 or block_table.shape[0] != B:
+        raise MlaError("block_table must be [B, max_pages]", MLA_ERR_INVALID_ARG)
+
+
+def mla_cache_append_q8(dims: MlaDims, c_kv, k_r, rope_cos, rope_sin, block_table, start_pos,
+                        cache, new_lens=None, dev_error=None, stream=None) -> None:
+    """Quantise c_kv [B, n, r] (e4m3, a power-of-two scale per 64 columns) and write it with
+    RoPE(k_r [B, n, G, d_r]) into the 8-bit cache [P, mla_q8_page_bytes] in place; sequence b
+    appends its first new_lens[b] tokens (all n without new_lens)."""
+    if not isinstance(c_kv, torch.Tensor) or c_kv.dim() != 3:
+        raise MlaError("c_kv must be a tensor [B, n, r]", MLA_ERR_INVALID_ARG)
+    B, n = c_kv.shape[0], c_kv.shape[1]
+    G, dr, r = dims.num_kv_groups, dims.rope_dim, dims.kv_lora_rank
+    _need(c_kv, "c_kv", torch.bfloat16, (B, n, r))
+    if dr > 0:
+        _need(k_r, "k_r", torch.bfloat16, (B, n, G, dr))
+        _need(rope_cos, "rope_cos", torch.float32, (B, n, G, dr // 2))
+        _need(rope_sin, "rope_sin", torch.float32, (B, n, G, dr // 2))
+    else:
+        k_r = rope_cos = rope_sin = None
+    _need_q8(dims, cache, block_table, B)
+    _need(start_pos, "start_pos", torch.int32, (B,))
+    if new_lens is not None:
+        _need(new_lens, "new_lens", torch.int32, (B,))
+    if dev_error is not None:
+        _need(dev_error, "dev_error", torch.int32)
+    with _one_device((c_kv, k_r, rope_cos, rope_sin, block_table, start_pos, cache, new_lens,
+                      dev_error), stream):
+        st = lib().mla_cache_append_q8(ctypes.byref(dims), _ptr(c_kv), _ptr(k_r), _ptr(rope_cos),
+                                       _ptr(rope_sin), _ptr(block_table), block_table.shape[1],
+                                       _ptr(start_pos), _ptr(new_lens), B, n, _ptr(cache),
+                                       cache.shape[0], _ptr(dev_error), _stream(stream))
+    _check(st, "mla_cache_append_q8")
+
+
+def mla_cache_read_q8(dims: MlaDims, cache, block_table, start_pos, out, read_lens=None,
+                      dev_error=None, stream=None) -> None:
+    """out [B, n, D] (bf16): rows start_pos[b] .. start_pos[b] + n - 1 of the 8-bit cache, exact;
+    rows at and past read_lens[b], if given, are left as they were."""
+    if not isinstance(out, torch.Tensor) or out.dim() != 3:
+        raise MlaError("out must be a tensor [B, n, D]", MLA_ERR_INVALID_ARG)
+    B, n = out.shape[0], out.shape[1]
+    _need(out, "out", torch.bfloat16, (B, n, dims.row_width))
+    _need_q8(dims, cache, block_table, B)
+    _need(start_pos, "start_pos", torch.int32, (B,))
+    if read_lens is not None:
+        _need(read_lens, "read_lens", torch.int32, (B,))
+    if dev_error is not None:
+        _need(dev_error, "dev_error", torch.int32)
+    with _one_device((cache, block_table, start_pos, out, read_lens, dev_error), stream):
+        st = lib().mla_cache_read_q8(ctypes.byref(dims), _ptr(cache), cache.shape[0],
+                                     _ptr(block_table), block_table.shape[1], _ptr(start_pos),
+                                     _ptr(read_lens), B, n, _ptr(out), _ptr(dev_error),
+                                     _stream(stream))
+    _check(st, "mla_cache_read_q8")
+
+
+def mla_decode_attn_q8(dims: MlaDims, q_ext, cache, block_table, seq_lens, max_seq_len: int,
+                       workspace, o_latent, lse, causal: bool = True, num_splits: int = 0,
+                       stream=None) -> None:
+    """mla_decode_attn over the 8-bit cache [P, mla_q8_page_bytes]: o_latent [B, q, H, r] (bf16)
+    and lse [B, q, H] (fp32); the workspace is mla_decode_workspace_size's."""
+    if not isinstance(q_ext, torch.Tensor) or q_ext.dim() != 4:
+        raise MlaError("q_ext must be a tensor [B, q, H, D]", MLA_ERR_INVALID_ARG)
+    B, q = q_ext.shape[0], q_ext.shape[1]
+    H, r = dims.num_heads, dims.kv_lora_rank
+    _need(q_ext, "q_ext", torch.bfloat16, (B, q, H, dims.row_width))
+    _need_q8(dims, cache, block_table, B)
+    _need(seq_lens, "seq_lens", torch.int32, (B,))
+    _need(o_latent, "o_latent", torch.bfloat16, (B, q, H, r))
+    _need(lse, "lse", torch.float32, (B, q, H))
+    _need(workspace, "workspace", torch.uint8)
+    with _one_device((q_ext, cache, block_table, seq_lens, o_latent, lse, workspace), stream):
+        st = lib().mla_decode_attn_q8(ctypes.byref(dims), _ptr(q_ext), _ptr(cache), cache.shape[0],
+                                      _ptr(block_table), block_table.shape[1], _ptr(seq_lens), B,
+                                      q, int(max_seq_len), 1 if causal else 0, int(num_splits),
+                                      _ptr(workspace), workspace.numel(), _ptr(o_latent),
+                                      _ptr(lse), _stream(stream))
+    _check(st, "mla_decode_attn_q8")
+
+
 def mla_kv_shared_decode_dims(dims: MlaDims) -> MlaDims:
     """Decode view of a K = V layout: the whole cache row is the latent (rank D, no rotary
     slot), so mla_decode_attn with these dims returns o_latent = sum_l p_l row_l."""
@@ -468,4 +590,6 @@ __all__ = ["MlaDims", "MlaError", "make_dims", "lib", "mla_row_width", "mla_cach
            "mla_decode_attn_noalloc", "mla_kv_shared_decode_dims", "mla_kv_shared_query",
            "mla_kv_shared_output", "mla_down_kv_append",
            "mla_out_proj_workspace_size",
-           "mla_out_proj", "mla_get_device_status", "mla_decode_step", "C_SYMBOLS", "STATUS_NAMES"]
+           "mla_out_proj", "mla_get_device_status", "mla_decode_step", "mla_q8_page_bytes",
+           "mla_cache_append_q8", "mla_cache_read_q8", "mla_decode_attn_q8", "C_SYMBOLS",
+           "STATUS_NAMES"]

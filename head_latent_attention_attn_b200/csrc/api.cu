@@ -8,6 +8,7 @@
 #include "host_common.h"
 #include "kernels.h"
 #include "ptx.cuh"
+#include "q8.cuh"
 
 using namespace mla;
 
@@ -579,17 +580,28 @@ size_t mla_decode_workspace_size(const mla_dims* dims, int32_t batch, int32_t q_
 
 namespace {
 
-// Validation, plan and parameters of mla_decode_attn (tensor maps encoded); *empty is set
-// when there is nothing to do.
+// Dims an 8-bit cache can have: 64-token pages, whole 64-column blocks, at most 8 of them.
+mla_status check_q8(const mla_dims* d) {
+  const mla_status st = check_dims(d);
+  if (st != MLA_OK) return st;
+  if (d->page_size != kQ8Tok || d->kv_lora_rank % kQ8Cols != 0 ||
+      d->kv_lora_rank > kQ8Cols * kQ8MaxBlocks)
+    return MLA_ERR_UNSUPPORTED;
+  return MLA_OK;
+}
+
+// Validation, plan and parameters of mla_decode_attn, or with q8 of mla_decode_attn_q8 (tensor
+// maps encoded); *empty is set when there is nothing to do.
 mla_status build_decode(const mla_dims* dims, const void* q_ext, const void* cache,
                         int64_t num_pages, const int32_t* block_table, int32_t max_pages_per_seq,
                         const int32_t* seq_lens, int32_t batch, int32_t q_len,
                         int32_t max_seq_len, int32_t causal, int32_t num_splits, void* workspace,
                         size_t workspace_bytes, void* o_latent, float* lse, DecodePlan* Pout,
-                        DecodeParams* pout, bool* empty, bool encode = true) {
+                        DecodeParams* pout, bool* empty, bool encode = true, bool q8 = false) {
   DecodePlan& P = *Pout;
   mla_status st = plan_decode(dims, batch, q_len, max_seq_len, num_splits, &P);
   if (st != MLA_OK) return st;
+  if (q8 && (st = check_q8(dims)) != MLA_OK) return st;
   if (num_pages <= 0 || num_pages * kDecodeTok > (int64_t(1) << 31) || max_pages_per_seq <= 0 ||
       (causal != 0 && causal != 1))
     return MLA_ERR_INVALID_ARG;
@@ -605,7 +617,7 @@ mla_status build_decode(const mla_dims* dims, const void* q_ext, const void* cac
   const int64_t qH = int64_t(q_len) * dims->num_heads;
   DecodeParams& p = *pout;
   p = DecodeParams{};
-  {
+  if (!q8) {
     const uint64_t d2[2] = {uint64_t(D), uint64_t(num_pages) * kDecodeTok};
     const uint64_t s2[1] = {uint64_t(D) * 2};
     const uint32_t box[2] = {64, uint32_t(kDecodeTok)};
@@ -619,14 +631,28 @@ mla_status build_decode(const mla_dims* dims, const void* q_ext, const void* cac
     if (!encode_bf16_map(&p.tm_q, q_ext, 3, d3, s3, box, CU_TENSOR_MAP_SWIZZLE_128B))
       return MLA_ERR_CUDA;
   }
-  if (P.pair) {
+  const uint32_t rope_cols = P.pair ? uint32_t(P.rope_half) : 64u;
+  const CUtensorMapSwizzle rope_sw = rope_cols == 64   ? CU_TENSOR_MAP_SWIZZLE_128B
+                                     : rope_cols == 32 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                                       : CU_TENSOR_MAP_SWIZZLE_32B;
+  const int r = dims->kv_lora_rank, R = D - r;
+  if (q8) {
+    p.cache_q8 = cache;
+    if (R > 0) {
+      const uint64_t d3[3] = {uint64_t(R), uint64_t(kDecodeTok), uint64_t(num_pages)};
+      const uint64_t s3[2] = {uint64_t(R) * 2, uint64_t(q8_page_bytes(r, R))};
+      const uint32_t box[3] = {rope_cols, uint32_t(kDecodeTok), 1};
+      if (!encode_bf16_map(&p.tm_rope, static_cast<const uint8_t*>(cache) + q8_keys_offset(r), 3,
+                           d3, s3, box, rope_sw))
+        return MLA_ERR_CUDA;
+    }
+  } else if (P.pair) {
     const uint64_t d2[2] = {uint64_t(D), uint64_t(num_pages) * kDecodeTok};
     const uint64_t s2[1] = {uint64_t(D) * 2};
-    const uint32_t box[2] = {uint32_t(P.rope_half), uint32_t(kDecodeTok)};
-    const CUtensorMapSwizzle sw = P.rope_half == 64   ? CU_TENSOR_MAP_SWIZZLE_128B
-                                  : P.rope_half == 32 ? CU_TENSOR_MAP_SWIZZLE_64B
-                                                      : CU_TENSOR_MAP_SWIZZLE_32B;
-    if (!encode_bf16_map(&p.tm_rope, cache, 2, d2, s2, box, sw)) return MLA_ERR_CUDA;
+    const uint32_t box[2] = {rope_cols, uint32_t(kDecodeTok)};
+    if (!encode_bf16_map(&p.tm_rope, cache, 2, d2, s2, box, rope_sw)) return MLA_ERR_CUDA;
+  }
+  if (P.pair) {
     p.q_ext = static_cast<const uint16_t*>(q_ext);
     p.rope_half = P.rope_half;
   }
@@ -715,6 +741,92 @@ mla_status mla_decode_attn(const mla_dims* dims, const void* q_ext, const void* 
                                      lse, &P, &p, &empty);
   if (st != MLA_OK || empty) return st;
   return launch_decode_plan(P, p, as_stream(stream));
+}
+
+mla_status mla_decode_attn_q8(const mla_dims* dims, const void* q_ext, const void* cache,
+                              int64_t num_pages, const int32_t* block_table,
+                              int32_t max_pages_per_seq, const int32_t* seq_lens, int32_t batch,
+                              int32_t q_len, int32_t max_seq_len, int32_t causal,
+                              int32_t num_splits, void* workspace, size_t workspace_bytes,
+                              void* o_latent, float* lse, void* stream) {
+  DecodePlan P;
+  DecodeParams p;
+  bool empty = false;
+  const mla_status st = build_decode(dims, q_ext, cache, num_pages, block_table,
+                                     max_pages_per_seq, seq_lens, batch, q_len, max_seq_len,
+                                     causal, num_splits, workspace, workspace_bytes, o_latent,
+                                     lse, &P, &p, &empty, true, true);
+  if (st != MLA_OK || empty) return st;
+  return launch_decode_plan(P, p, as_stream(stream));
+}
+
+int64_t mla_q8_page_bytes(const mla_dims* dims) {
+  if (check_q8(dims) != MLA_OK) return -1;
+  return q8_page_bytes(dims->kv_lora_rank, dims->num_kv_groups * dims->rope_dim);
+}
+
+mla_status mla_cache_append_q8(const mla_dims* dims, const void* c_kv, const void* k_r,
+                               const float* rope_cos, const float* rope_sin,
+                               const int32_t* block_table, int32_t max_pages_per_seq,
+                               const int32_t* start_pos, const int32_t* new_lens, int32_t batch,
+                               int32_t n_new, void* cache, int64_t num_pages, int32_t* dev_error,
+                               void* stream) {
+  const mla_status st = check_q8(dims);
+  if (st != MLA_OK) return st;
+  if (batch < 0 || n_new < 0 || max_pages_per_seq <= 0 || num_pages <= 0 ||
+      num_pages > INT32_MAX)
+    return MLA_ERR_INVALID_ARG;
+  if (batch == 0 || n_new == 0) return MLA_OK;
+  if (!c_kv || !block_table || !start_pos || !cache) return MLA_ERR_INVALID_ARG;
+  if (dims->rope_dim > 0 && (!k_r || !rope_cos || !rope_sin)) return MLA_ERR_INVALID_ARG;
+  if (!aligned(c_kv, 16) || !aligned(cache, 16)) return MLA_ERR_INVALID_ARG;
+  if (int64_t(batch) * n_new > int64_t(INT32_MAX) * 8) return MLA_ERR_UNSUPPORTED;
+  AppendQ8Params p{};
+  p.c_kv = static_cast<const uint16_t*>(c_kv);
+  p.k_r = static_cast<const uint16_t*>(k_r);
+  p.rope_cos = rope_cos;
+  p.rope_sin = rope_sin;
+  p.block_table = block_table;
+  p.start_pos = start_pos;
+  p.new_lens = new_lens;
+  p.cache = static_cast<uint8_t*>(cache);
+  p.dev_error = dev_error;
+  p.num_pages = num_pages;
+  p.max_pages = max_pages_per_seq;
+  p.batch = batch;
+  p.n_new = n_new;
+  p.r = dims->kv_lora_rank;
+  p.groups = dims->num_kv_groups;
+  p.rope_dim = dims->rope_dim;
+  return launch_cache_append_q8(p, as_stream(stream)) == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+}
+
+mla_status mla_cache_read_q8(const mla_dims* dims, const void* cache, int64_t num_pages,
+                             const int32_t* block_table, int32_t max_pages_per_seq,
+                             const int32_t* start_pos, const int32_t* read_lens, int32_t batch,
+                             int32_t n, void* out, int32_t* dev_error, void* stream) {
+  const mla_status st = check_q8(dims);
+  if (st != MLA_OK) return st;
+  if (batch < 0 || n < 0 || max_pages_per_seq <= 0 || num_pages <= 0 || num_pages > INT32_MAX)
+    return MLA_ERR_INVALID_ARG;
+  if (batch == 0 || n == 0) return MLA_OK;
+  if (!cache || !block_table || !start_pos || !out) return MLA_ERR_INVALID_ARG;
+  if (!aligned(cache, 16) || !aligned(out, 16)) return MLA_ERR_INVALID_ARG;
+  if (int64_t(batch) * ((int64_t(n) + 7) / 8) > int64_t(INT32_MAX) * 8) return MLA_ERR_UNSUPPORTED;
+  ReadQ8Params p{};
+  p.cache = static_cast<const uint8_t*>(cache);
+  p.block_table = block_table;
+  p.start_pos = start_pos;
+  p.read_lens = read_lens;
+  p.out = static_cast<uint16_t*>(out);
+  p.dev_error = dev_error;
+  p.num_pages = num_pages;
+  p.max_pages = max_pages_per_seq;
+  p.batch = batch;
+  p.n = n;
+  p.r = dims->kv_lora_rank;
+  p.R = dims->num_kv_groups * dims->rope_dim;
+  return launch_cache_read_q8(p, as_stream(stream)) == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }
 
 mla_status mla_decode_step(const mla_dims* dims, const void* c_kv_new, const void* k_r_new,

@@ -1,13 +1,34 @@
 // append.cuh - one new token's cache row, written by one warp: the latent row moves as
 // 16-byte vectors, the rotary pairs are rotated in fp32 (separately rounded multiply /
 // subtract / add) and rounded to bf16 with ties to even. Used by cache_append_kernel and,
-// folded into the query absorption, by the one-call decode step.
+// folded into the query absorption, by the one-call decode step; the rotation also by the
+// 8-bit cache's append.
 #pragma once
 
 #include "kernels.h"
 #include "ptx.cuh"
 
 namespace mla {
+
+// Rotary key of every group of one token, one pair (x_j, x_{j + d_r/2}) per lane and step:
+// fp32 with separately rounded products and sums, then bf16 with ties to even.
+MLA_DEVICE void rotate_keys(const uint16_t* kr, const float* cs, const float* sn, int groups,
+                            int rope_dim, int lane, uint16_t* dst) {
+  const int half = rope_dim / 2;
+  const int npairs = groups * half;
+  for (int idx = lane; idx < npairs; idx += 32) {
+    const int g = idx / half;
+    const int j = idx - g * half;
+    const float x0 = bf16_bits_to_f32(kr[g * rope_dim + j]);
+    const float x1 = bf16_bits_to_f32(kr[g * rope_dim + j + half]);
+    const float c = cs[idx];
+    const float s = sn[idx];
+    const float y0 = __fsub_rn(__fmul_rn(x0, c), __fmul_rn(x1, s));
+    const float y1 = __fadd_rn(__fmul_rn(x1, c), __fmul_rn(x0, s));
+    dst[g * rope_dim + j] = f32_to_bf16_rne(y0);
+    dst[g * rope_dim + j + half] = f32_to_bf16_rne(y1);
+  }
+}
 
 // Token gw = b * n_new + t of the batch (0 <= gw < batch * n_new); all 32 lanes call it.
 MLA_DEVICE void append_token(const AppendParams& p, int64_t gw, int lane) {
@@ -32,24 +53,9 @@ MLA_DEVICE void append_token(const AppendParams& p, int64_t gw, int lane) {
   uint4* dst4 = reinterpret_cast<uint4*>(dst);
   for (int i = lane; i < p.r / 8; i += 32) dst4[i] = src4[i];
 
-  // rotary key of every group
-  const int half = p.rope_dim / 2;
-  const int npairs = p.groups * half;
-  const uint16_t* kr = p.k_r + gw * int64_t(p.groups) * p.rope_dim;
-  const float* cs = p.rope_cos + gw * npairs;
-  const float* sn = p.rope_sin + gw * npairs;
-  for (int idx = lane; idx < npairs; idx += 32) {
-    const int g = idx / half;
-    const int j = idx - g * half;
-    const float x0 = bf16_bits_to_f32(kr[g * p.rope_dim + j]);
-    const float x1 = bf16_bits_to_f32(kr[g * p.rope_dim + j + half]);
-    const float c = cs[idx];
-    const float s = sn[idx];
-    const float y0 = __fsub_rn(__fmul_rn(x0, c), __fmul_rn(x1, s));
-    const float y1 = __fadd_rn(__fmul_rn(x1, c), __fmul_rn(x0, s));
-    dst[p.r + g * p.rope_dim + j] = f32_to_bf16_rne(y0);
-    dst[p.r + g * p.rope_dim + j + half] = f32_to_bf16_rne(y1);
-  }
+  const int64_t npairs = int64_t(p.groups) * (p.rope_dim / 2);
+  rotate_keys(p.k_r + gw * 2 * npairs, p.rope_cos + gw * npairs, p.rope_sin + gw * npairs,
+              p.groups, p.rope_dim, lane, dst + p.r);
 }
 
 }  // namespace mla

@@ -36,6 +36,7 @@
 #include "decode_sched.cuh"
 #include "kernels.h"
 #include "ptx.cuh"
+#include "q8.cuh"
 
 namespace mla {
 
@@ -59,6 +60,13 @@ __device__ unsigned long long g_mla_trace[10 * kTraceTiles + 1];
 namespace {
 
 constexpr int kThreads = 224;
+// Warps that dequantise pages of the 8-bit cache (Q8 only). Eight give each of them one 8-token
+// group of a page; with 64 query columns the softmax warps need the registers, so four take
+// two groups each.
+template <int NCOL>
+constexpr int kDequantWarps = NCOL == 64 ? 4 : 8;
+template <int NCOL, bool Q8>
+constexpr int kBlockThreads = kThreads + (Q8 ? 32 * kDequantWarps<NCOL> : 0);
 constexpr int kBlkBytes = kDecodeTok * 128;   // one 64 x 64 bf16 block, 8 KB
 constexpr float kLazyThreshold = 8.0f;        // log2 units
 // Initial reference max: finite, so a masked score (-inf) minus it is exactly -inf (weight
@@ -161,8 +169,8 @@ size_t decode_smem_bytes(int ncol, int nblk, int slot_blocks, int nslot, int npt
   return decode_layout(ncol, nblk, slot_blocks, nslot, npt).total;
 }
 
-template <int NCOL>
-__global__ void __launch_bounds__(kThreads, 1)
+template <int NCOL, bool Q8>
+__global__ void __launch_bounds__(kBlockThreads<NCOL, Q8>, 1)
     mla_decode_kernel(const __grid_constant__ DecodeParams p) {
   constexpr int HALF = NCOL / 2;
   extern __shared__ uint8_t smem_raw[];
@@ -179,7 +187,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(misc + 8);
   volatile int* abort_flag = misc + 9;
   int* sched = misc + 10;                              // b_a, s_a, r0, r1, per, scan carry
-  int* warp_sum = misc + 16;                           // [6]
+  // one int per warp while the schedule is made; the softmax's `red` is unused until then over
+  int* warp_sum = Q8 ? reinterpret_cast<int*>(red) : misc + 16;
   int* chg_flag = misc + 23;                           // [2] reference moved, per half
   static_assert(23 + 2 <= kMiscInts, "misc ints overflow into the mbarriers");
   uint64_t* bars = reinterpret_cast<uint64_t*>(base + lay.bar_off);
@@ -207,7 +216,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < p.nslot; ++s) {
-      mbar_init(&full[s], 1);
+      mbar_init(&full[s], Q8 ? 1 + kDequantWarps<NCOL> : 1);
       mbar_init(&empty[s], 1);
     }
     mbar_init(q_full, 1);
@@ -232,7 +241,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // ---- schedule: this CTA's tile range [r0, r1) in its row block, first sequence -------
   // The row blocks of a sequence are worked on in lockstep by neighbouring CTAs, so the
   // second read of every page is served from L2.
-  find_tile_range<kThreads>(p, vc, vgrid, blockIdx.x == 0, warp_sum, sched);
+  find_tile_range<kBlockThreads<NCOL, Q8>>(p, vc, vgrid, blockIdx.x == 0, warp_sum, sched);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -243,7 +252,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 0) {
     // ===================================== TMA producer ==================================
     if (has_work && elect_one()) {
-      prefetch_tensormap(&p.tm_cache);
+      prefetch_tensormap(Q8 ? &p.tm_rope : &p.tm_cache);
       prefetch_tensormap(&p.tm_q);
       if (blockIdx.x == 0) *p.range_len = per;
       UnitWalk w{sched[0], sched[1]};
@@ -274,9 +283,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           uint8_t* sbase = slots + slot * slot_bytes;
           uint64_t* fb = &full[slot];
-          mbar_arrive_expect_tx(fb, uint32_t(p.nblk) * kBlkBytes);
-          for (int k = 0; k < p.nblk; ++k)
-            tma_load_2d(sbase + k * kBlkBytes, &p.tm_cache, k * 64, page * kDecodeTok, fb);
+          if constexpr (Q8) {
+            // the rotated keys only; the latent blocks come from the dequantising warps
+            const int lb = p.r / kQ8Cols;
+            mbar_arrive_expect_tx(fb, uint32_t(p.nblk - lb) * kBlkBytes);
+            for (int k = lb; k < p.nblk; ++k)
+              tma_load_3d(sbase + k * kBlkBytes, &p.tm_rope, (k - lb) * 64, 0, page, fb);
+          } else {
+            mbar_arrive_expect_tx(fb, uint32_t(p.nblk) * kBlkBytes);
+            for (int k = 0; k < p.nblk; ++k)
+              tma_load_2d(sbase + k * kBlkBytes, &p.tm_cache, k * 64, page * kDecodeTok, fb);
+          }
           MLA_TRACE_AT(8, jj);
         }
       }
@@ -379,6 +396,83 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     __syncwarp();
+  } else if (Q8 && warp >= 7) {
+    // ============================== dequantising warps (Q8) ==============================
+    // Each 8-token group of a page is one warp's (lane: token lane / 4, 16 of the 64 columns
+    // of every block). The next page's codes are loaded into registers as this page's leave
+    // them, so a whole page per CTA is always on its way from memory without shared memory to
+    // hold it, and the page takes no trip through shared memory as codes.
+    if (has_work) {
+      constexpr int NG = 8 / kDequantWarps<NCOL>;       // 8-token groups of this warp
+      const int lb = p.r / kQ8Cols;
+      const int part = lane & 3;
+      const int64_t page_bytes = q8_page_bytes(p.r, p.D - p.r);
+      const int sc_off = q8_scales_offset(p.r, p.D - p.r);
+      uint4 codes[NG][kQ8MaxBlocks];
+      uint2 scales[NG];
+      UnitWalk w{sched[0], sched[1]};
+      w.load(p, cg);
+      int t = r0;
+      // codes and scales of this warp's tokens in tile t; zero codes past the context, whose
+      // rows must not reach O^T (0-weight x garbage)
+      auto fetch = [&]() {
+        int32_t page = p.block_table[int64_t(w.b) * p.max_pages + (t - w.s)];
+        if (page < 0 || page >= p.num_pages) page = 0;   // the producer reports it
+        const uint8_t* src = static_cast<const uint8_t*>(p.cache_q8) + page * page_bytes;
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+          const int tok = 8 * ((warp - 7) * NG + g) + (lane >> 2);
+          const bool live = (t - w.s) * kDecodeTok + tok < w.L;
+          scales[g] = live ? *reinterpret_cast<const uint2*>(src + sc_off + tok * kQ8ScaleBytes)
+                           : make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
+#pragma unroll
+          for (int k = 0; k < kQ8MaxBlocks; ++k)
+            codes[g][k] = (k < lb && live) ? ld_stream_v4(src + k * kQ8BlockBytes + tok * kQ8Cols +
+                                                          16 * part)
+                                           : make_uint4(0, 0, 0, 0);
+        }
+      };
+      fetch();
+      SlotRing ring(p.nslot);
+      for (int jj = 0;; ++jj, ring.next()) {
+        if (jj >= p.nslot &&
+            !__all_sync(0xffffffffu, mbar_wait(&empty[ring.slot], (ring.round - 1) & 1, wc)))
+          break;
+        uint8_t* sbase = slots + ring.slot * slot_bytes;
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+          const int tok = 8 * ((warp - 7) * NG + g) + (lane >> 2);
+          uint8_t* rowp = sbase + tok * 128;
+#pragma unroll
+          for (int k = 0; k < kQ8MaxBlocks; ++k) {
+            if (k >= lb) break;
+            const uint32_t s = ((k < 4 ? scales[g].x : scales[g].y) >> (8 * (k & 3))) & 0xFFu;
+            uint32_t v[8];
+            q8_decode16(codes[g][k], q8_factor(s), v);
+            if (s > kQ8OneFactorMax) {
+              const uint32_t f2 = q8_factor2(s);
+#pragma unroll
+              for (int i = 0; i < 8; ++i) v[i] = mul_bf16x2(v[i], f2);
+            }
+            uint8_t* blk = rowp + k * kBlkBytes;
+            *reinterpret_cast<uint4*>(blk + (((2 * part) ^ (tok & 7)) << 4)) =
+                make_uint4(v[0], v[1], v[2], v[3]);
+            *reinterpret_cast<uint4*>(blk + (((2 * part + 1) ^ (tok & 7)) << 4)) =
+                make_uint4(v[4], v[5], v[6], v[7]);
+          }
+        }
+        if (++t == w.s + w.tiles) {                      // on to the next unit
+          w.s += w.tiles;
+          ++w.b;
+          if (t < r1) w.load(p, cg);
+        }
+        if (t < r1) fetch();
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&full[ring.slot]);
+        if (t >= r1) break;
+      }
+    }
   } else if (has_work) {   // warps 2-5
     // ================================ softmax, epilogue ==================================
     const int sp = warp & 3;                  // TMEM sub-partition this warp may access
@@ -537,7 +631,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         // cache rows past the context may hold anything (even NaN): zero them so that
         // 0-weight x garbage cannot reach O^T
-        if (pos >= L) {
+        if (!Q8 && pos >= L) {
           uint8_t* sbase = slots + slot * slot_bytes;
           for (int k = hf; k < 2 * p.nch; k += 2) {
             uint4* rowp = reinterpret_cast<uint4*>(sbase + k * kBlkBytes + tok * 128);
@@ -636,21 +730,29 @@ extern "C" int mla_trace_read(unsigned long long* host, int n) {
 #endif
 
 
-template <int NCOL>
+template <int NCOL, bool Q8>
 static cudaError_t launch_decode_n(const DecodeParams& p, dim3 grid, size_t smem,
                                    cudaStream_t stream) {
-  cudaError_t e = cudaFuncSetAttribute(mla_decode_kernel<NCOL>,
+  cudaError_t e = cudaFuncSetAttribute(mla_decode_kernel<NCOL, Q8>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
   if (e != cudaSuccess) return e;
-  return launch_pdl(mla_decode_kernel<NCOL>, grid, dim3(kThreads), smem, stream, 1, p);
+  return launch_pdl(mla_decode_kernel<NCOL, Q8>, grid, dim3(kBlockThreads<NCOL, Q8>), smem, stream,
+                    1, p);
 }
 
 cudaError_t launch_decode(const DecodeParams& p, int ncol, dim3 grid, size_t smem,
                           cudaStream_t stream) {
+  const bool q8 = p.cache_q8 != nullptr;
   switch (ncol) {
-    case 16: return launch_decode_n<16>(p, grid, smem, stream);
-    case 32: return launch_decode_n<32>(p, grid, smem, stream);
-    case 64: return launch_decode_n<64>(p, grid, smem, stream);
+    case 16:
+      return q8 ? launch_decode_n<16, true>(p, grid, smem, stream)
+                : launch_decode_n<16, false>(p, grid, smem, stream);
+    case 32:
+      return q8 ? launch_decode_n<32, true>(p, grid, smem, stream)
+                : launch_decode_n<32, false>(p, grid, smem, stream);
+    case 64:
+      return q8 ? launch_decode_n<64, true>(p, grid, smem, stream)
+                : launch_decode_n<64, false>(p, grid, smem, stream);
     default: return cudaErrorInvalidValue;
   }
 }

@@ -41,6 +41,7 @@
 #include "decode_sched.cuh"
 #include "kernels.h"
 #include "ptx.cuh"
+#include "q8.cuh"
 
 namespace mla {
 
@@ -68,8 +69,14 @@ __device__ unsigned long long g_mla_pair_trace[kPairTraceEvents * kPairTraceTile
 namespace {
 
 constexpr int kPvWarp = 2;
-constexpr int kRowWarp0 = 3;                                   // first of the 12 row warps
-constexpr int kThreads = 32 * (kRowWarp0 + 12);
+// First of the 12 row warps. Over the 8-bit cache (Q8) four more warps follow them, which
+// dequantise this CTA's half of each page, and the row warps start at 4 so that every role is
+// one aligned group of four warps and can take its own share of the registers.
+template <bool Q8>
+constexpr int kRowWarp0 = Q8 ? 4 : 3;
+template <bool Q8>
+constexpr int kThreads = 32 * (kRowWarp0<Q8> + 12 + (Q8 ? 4 : 0));
+constexpr int kDequantWarp0 = kRowWarp0<true> + 12;
 constexpr int kHalfTok = kDecodeTok / 2;                       // tokens per owner thread
 constexpr uint32_t kBlk = kDecodeTok * 128;                    // 64 x 64 bf16 block, 8 KB
 constexpr int kPackWords = kHalfTok * 3 / 4;                   // 24-bit values of a half row
@@ -241,7 +248,8 @@ size_t decode_pair_smem_bytes(int r, int rope_half, int nslot) {
   return pair_layout(r, rope_half, nslot).total;
 }
 
-__global__ void __launch_bounds__(kThreads, 1)
+template <bool Q8>
+__global__ void __launch_bounds__(kThreads<Q8>, 1)
     mla_decode_pair_kernel(const __grid_constant__ DecodeParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = align_1024(smem_raw);
@@ -257,7 +265,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int* abort_flag = misc + 1;
   int* sched = misc + 2;
   int* warp_sum = misc + 8;
-  static_assert(8 + kThreads / 32 <= kMiscInts, "misc ints overflow into the mbarriers");
+  static_assert(8 + kThreads<Q8> / 32 <= kMiscInts, "misc ints overflow into the mbarriers");
   uint64_t* bars = reinterpret_cast<uint64_t*>(base + lay.bar_off);
   // One barrier per slot for all of a page's TMA boxes: the S issuer needs every box before
   // it starts, and each mbarrier operation here costs a few hundred cycles of latency.
@@ -286,7 +294,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < p.nslot; ++s) {
-      mbar_init(&full[s], 1);
+      mbar_init(&full[s], Q8 ? 1 + 4 : 1);             // the TMA producer, 4 dequantising warps
       mbar_init(&empty[s], 1);
     }
     mbar_init(q_full, 8);                              // 4 owner + 4 sender warps
@@ -315,7 +323,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   grid_dep_wait();
   grid_dep_launch();
   // Both CTAs of the cluster compute the same range (same pair index).
-  find_tile_range<kThreads>(p, vc, vgrid, blockIdx.x == 0, warp_sum, sched);
+  find_tile_range<kThreads<Q8>>(p, vc, vgrid, blockIdx.x == 0, warp_sum, sched);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -332,7 +340,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 0) {
     // ===================================== TMA producer ==================================
     if (has_work && elect_one()) {
-      prefetch_tensormap(&p.tm_cache);
+      if (!Q8) prefetch_tensormap(&p.tm_cache);
       prefetch_tensormap(&p.tm_rope);
       if (blockIdx.x == 0) *p.range_len = per;
       UnitWalk w{sched[0], sched[1]};
@@ -358,12 +366,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           uint8_t* sbase = slots + slot * lay.slot_bytes;
           uint64_t* fb = &full[slot];
-          mbar_arrive_expect_tx(fb, uint32_t(lb) * kBlk + rope_bytes);
-          for (int k = 0; k < lb; ++k)
-            tma_load_2d(sbase + k * kBlk, &p.tm_cache, int(rank) * rhalf + k * 64,
-                        page * kDecodeTok, fb);
-          tma_load_2d(sbase + lay.rope_off, &p.tm_rope, r + int(rank) * rh, page * kDecodeTok,
-                      fb);
+          if constexpr (Q8) {
+            mbar_arrive_expect_tx(fb, rope_bytes);
+            tma_load_3d(sbase + lay.rope_off, &p.tm_rope, int(rank) * rh, 0, page, fb);
+          } else {
+            mbar_arrive_expect_tx(fb, uint32_t(lb) * kBlk + rope_bytes);
+            for (int k = 0; k < lb; ++k)
+              tma_load_2d(sbase + k * kBlk, &p.tm_cache, int(rank) * rhalf + k * 64,
+                          page * kDecodeTok, fb);
+            tma_load_2d(sbase + lay.rope_off, &p.tm_rope, r + int(rank) * rh, page * kDecodeTok,
+                        fb);
+          }
           MLA_PTRACE(0, jj);
         }
       }
@@ -465,13 +478,90 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     __syncwarp();
+  } else if (Q8 && warp >= kDequantWarp0) {
+    // ============================== dequantising warps (Q8) ==============================
+    // This CTA's r/2 latent columns of each page, as in the one-CTA kernel (decode.cu): two
+    // 8-token groups a warp, the next page's codes loaded as this page's leave the registers.
+    if (has_work) {
+      constexpr int NG = 2;
+      constexpr int kHalfBlocks = kQ8MaxBlocks / 2;
+      const int part = lane & 3;
+      const int64_t page_bytes = q8_page_bytes(r, p.D - r);
+      const int sc_off = q8_scales_offset(r, p.D - r);
+      uint4 codes[NG][kHalfBlocks];
+      uint32_t scales[NG];                               // of this CTA's blocks, a byte each
+      UnitWalk w{sched[0], sched[1]};
+      w.load(p, cg);
+      int t = r0;
+      auto fetch = [&]() {
+        int32_t page = p.block_table[int64_t(w.b) * p.max_pages + (t - w.s)];
+        if (page < 0 || page >= p.num_pages) page = 0;   // the producer reports it
+        const uint8_t* src = static_cast<const uint8_t*>(p.cache_q8) + page * page_bytes;
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+          const int tok = 8 * ((warp - kDequantWarp0) * NG + g) + (lane >> 2);
+          const bool live = (t - w.s) * kDecodeTok + tok < w.L;
+          uint2 sc = make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
+          if (live) sc = *reinterpret_cast<const uint2*>(src + sc_off + tok * kQ8ScaleBytes);
+          scales[g] = uint32_t((uint64_t(sc.y) << 32 | sc.x) >> (8 * lb * int(rank)));
+#pragma unroll
+          for (int k = 0; k < kHalfBlocks; ++k)
+            codes[g][k] = (k < lb && live)
+                              ? ld_stream_v4(src + (int(rank) * lb + k) * kQ8BlockBytes +
+                                             tok * kQ8Cols + 16 * part)
+                              : make_uint4(0, 0, 0, 0);
+        }
+      };
+      fetch();
+      SlotRing ring(p.nslot);
+      for (int jj = 0;; ++jj, ring.next()) {
+        if (jj >= p.nslot &&
+            !__all_sync(0xffffffffu, mbar_wait(&empty[ring.slot], (ring.round - 1) & 1, wc)))
+          break;
+        uint8_t* sbase = slots + ring.slot * lay.slot_bytes;
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+          const int tok = 8 * ((warp - kDequantWarp0) * NG + g) + (lane >> 2);
+          uint8_t* rowp = sbase + tok * 128;
+#pragma unroll
+          for (int k = 0; k < kHalfBlocks; ++k) {
+            if (k >= lb) break;
+            const uint32_t s = (scales[g] >> (8 * k)) & 0xFFu;
+            uint32_t v[8];
+            q8_decode16(codes[g][k], q8_factor(s), v);
+            if (s > kQ8OneFactorMax) {
+              const uint32_t f2 = q8_factor2(s);
+#pragma unroll
+              for (int i = 0; i < 8; ++i) v[i] = mul_bf16x2(v[i], f2);
+            }
+            uint8_t* blk = rowp + k * kBlk;
+            *reinterpret_cast<uint4*>(blk + (((2 * part) ^ (tok & 7)) << 4)) =
+                make_uint4(v[0], v[1], v[2], v[3]);
+            *reinterpret_cast<uint4*>(blk + (((2 * part + 1) ^ (tok & 7)) << 4)) =
+                make_uint4(v[4], v[5], v[6], v[7]);
+          }
+        }
+        if (++t == w.s + w.tiles) {                      // on to the next unit
+          w.s += w.tiles;
+          ++w.b;
+          if (t < r1) w.load(p, cg);
+        }
+        if (t < r1) fetch();
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&full[ring.slot]);
+        if (t >= r1) break;
+      }
+    }
+  } else if (Q8 && warp == 3) {
+    // spare: fills the issuers' group of four warps
   } else if (has_work) {
     // ==================================== the 128 rows ====================================
     // Every row warp works on 16 TMEM lanes of its sub-partition with 16x32bx2 accesses:
     // lanes i and i + 16 of the warp share row i and take tokens 0-31 and 32-63 (or the
     // two 16-column halves of every 32 columns of O).
     const int sp = warp & 3;                  // TMEM sub-partition this warp reaches
-    const int role = (warp - kRowWarp0) >> 2; // 0 owner, 1 sender, 2 receiver
+    const int role = (warp - kRowWarp0<Q8>) >> 2; // 0 owner, 1 sender, 2 receiver
     const int qt = lane >> 4;                 // token half of this thread
     const int i16 = lane & 15;
     // owners work on this CTA's rows, senders and receivers on the partner's
@@ -716,7 +806,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (tr) MLA_PTRACE(6, jj);
           // cache rows past the context may hold anything (even NaN): zero their latent half
           // so that 0-weight x garbage cannot reach O
-          if (tile_pos0 + kDecodeTok > L) {
+          if (!Q8 && tile_pos0 + kDecodeTok > L) {
             const int tid = sp * 32 + lane;      // 0..127
             const int tok = tid & (kDecodeTok - 1);
             if (tile_pos0 + tok >= L) {
@@ -869,7 +959,9 @@ extern "C" int mla_pair_trace_read(unsigned long long* host, int n) {
 #endif
 
 int decode_pair_max_clusters(size_t smem) {
-  if (cudaFuncSetAttribute(mla_decode_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  // one CTA per SM by its shared memory, over either cache
+  if (cudaFuncSetAttribute(mla_decode_pair_kernel<false>,
+                           cudaFuncAttributeMaxDynamicSharedMemorySize,
                            int(smem)) != cudaSuccess) {
     cudaGetLastError();
     return 0;
@@ -881,24 +973,31 @@ int decode_pair_max_clusters(size_t smem) {
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   cfg.gridDim = dim3(2);
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(kThreads<false>);
   cfg.dynamicSmemBytes = smem;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   int n = 0;
-  if (cudaOccupancyMaxActiveClusters(&n, mla_decode_pair_kernel, &cfg) != cudaSuccess) {
+  if (cudaOccupancyMaxActiveClusters(&n, mla_decode_pair_kernel<false>, &cfg) != cudaSuccess) {
     cudaGetLastError();
     return 0;
   }
   return n;
 }
 
-cudaError_t launch_decode_pair(const DecodeParams& p, dim3 grid, size_t smem,
-                               cudaStream_t stream) {
-  cudaError_t e = cudaFuncSetAttribute(mla_decode_pair_kernel,
+template <bool Q8>
+static cudaError_t launch_decode_pair_t(const DecodeParams& p, dim3 grid, size_t smem,
+                                        cudaStream_t stream) {
+  cudaError_t e = cudaFuncSetAttribute(mla_decode_pair_kernel<Q8>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
   if (e != cudaSuccess) return e;
-  return launch_pdl(mla_decode_pair_kernel, grid, dim3(kThreads), smem, stream, 2, p);
+  return launch_pdl(mla_decode_pair_kernel<Q8>, grid, dim3(kThreads<Q8>), smem, stream, 2, p);
+}
+
+cudaError_t launch_decode_pair(const DecodeParams& p, dim3 grid, size_t smem,
+                               cudaStream_t stream) {
+  return p.cache_q8 ? launch_decode_pair_t<true>(p, grid, smem, stream)
+                    : launch_decode_pair_t<false>(p, grid, smem, stream);
 }
 
 }  // namespace mla

@@ -54,6 +54,34 @@ struct AppendParams {
 };
 cudaError_t launch_cache_append(const AppendParams& p, cudaStream_t stream);
 
+// ---- the 8-bit latent cache: mla_cache_append_q8, mla_cache_read_q8 (layout: q8.cuh) -------
+struct AppendQ8Params {
+  const uint16_t* c_kv;      // [B, n_new, r]
+  const uint16_t* k_r;       // [B, n_new, G, d_r]
+  const float* rope_cos;     // [B, n_new, G, d_r/2]
+  const float* rope_sin;
+  const int32_t* block_table;
+  const int32_t* start_pos;
+  const int32_t* new_lens;   // [B] tokens to write of each sequence, or null: all n_new
+  uint8_t* cache;            // [num_pages, page bytes]
+  int32_t* dev_error;
+  int64_t num_pages;
+  int32_t max_pages, batch, n_new, r, groups, rope_dim;
+};
+cudaError_t launch_cache_append_q8(const AppendQ8Params& p, cudaStream_t stream);
+
+struct ReadQ8Params {
+  const uint8_t* cache;
+  const int32_t* block_table;
+  const int32_t* start_pos;
+  const int32_t* read_lens;  // [B] rows to read of each sequence, or null: all n
+  uint16_t* out;             // [B, n, r + R]
+  int32_t* dev_error;
+  int64_t num_pages;
+  int32_t max_pages, batch, n, r, R;
+};
+cudaError_t launch_cache_read_q8(const ReadQ8Params& p, cudaStream_t stream);
+
 // ---- the single-latent K = V form: rotary slice of the query / inverse rotation of o ---
 struct KvSharedParams {
   const uint16_t* in;        // [rows, r + d_r] bf16
@@ -153,8 +181,14 @@ struct DecodeParams {
   int32_t max_pages, batch, q_len, num_heads, qH, r, D, nblk, nch, col_groups, units,
       max_seq_len, causal, nslot, slot_blocks, tmem_cols, npt;
   float scale_log2;          // softmax_scale * log2(e)
+  // The 8-bit cache (q8.cuh): its pages, or null for the bf16 cache. tm_cache is then unused
+  // and tm_rope covers the pages' key planes, 3D {R, 64, num_pages}.
+  const void* cache_q8;
+  // rotary columns: the latent-split cluster kernel's over the bf16 cache, 2D {D, num_pages*64},
+  // box {rope_half, 64}; over the 8-bit cache box {rope_half, 64, 1} there and {64, 64, 1} in
+  // the one-CTA kernel
+  CUtensorMap tm_rope;
   // used by the latent-split cluster kernel only
-  CUtensorMap tm_rope;       // 2D {D, num_pages*64}, box {rope_half, 64}
   const uint16_t* q_ext;     // [B, q*H, D]
   int32_t rope_half;         // rotary columns per CTA of the pair (G*d_r/2)
 };

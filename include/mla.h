@@ -229,6 +229,61 @@ mla_status mla_decode_attn(const mla_dims* dims, const void* q_ext, const void* 
                            void* o_latent, float* lse, void* stream);
 
 /*
+ * The 8-bit latent cache. The same paged cache with c_kv held in 8 bits: half the bytes that a
+ * long context needs and that every decode step reads. The rotary keys stay bf16, since every
+ * score of every head depends on them and they are an eighth of the row.
+ *
+ * A cache page is mla_q8_page_bytes(dims) = 64 (r + 2 R + 8) bytes, R = G*d_r, for 64 tokens:
+ *   codes   [r/64][64 tokens][64]  e4m3 code of latent column 64 k + j of token t
+ *   keys    [64 tokens][R]         bf16, rotated keys of every group
+ *   scales  [64 tokens][8]         byte k: exponent + 127 of the token's column block k
+ * Block k of token t holds x = code * 2^(byte - 127), which is exact in bf16. The exponent is the
+ * least e in [-110, 119] with max|x| * 2^-e <= 448 over the block's 64 columns; the codes are
+ * round-to-nearest-even of x * 2^-e (beyond 448 * 2^119 they saturate). A block that holds an
+ * infinity or a NaN has byte 255 and reads back as NaN, all 64 columns of it.
+ * Requires page_size == 64, r % 64 == 0 and r <= 512 (MLA_ERR_UNSUPPORTED otherwise).
+ *
+ * mla_q8_page_bytes: bytes of a page, or -1 when `dims` cannot have an 8-bit cache.
+ *
+ * mla_cache_append_q8 - quantise new tokens into the cache; arguments as mla_cache_append, and
+ *   cache       uint8 [num_pages, mla_q8_page_bytes] updated in place, 16-byte aligned
+ *   new_lens    int32 [B] or NULL: sequence b appends its first new_lens[b] of the n_new tokens
+ *               (a padded batch; each in [0, n_new], else it appends none and
+ *               MLA_DEVERR_BOUNDS is set). NULL: all n_new.
+ *   The keys are the bits that mla_cache_append would write. Bounds faults as there.
+ *
+ * mla_cache_read_q8 - rows of the cache as bf16, what mla_cache_append's cache would hold for
+ * the quantised latents (to expand a context's keys and values, or to move it elsewhere).
+ *   start_pos   int32 [B]  position of the first row of sequence b
+ *   read_lens   int32 [B] or NULL: rows to read (in [0, n], else none and MLA_DEVERR_BOUNDS);
+ *               NULL: all n. Rows of `out` at and past read_lens[b] are left as they were.
+ *   out         bf16 [B, n, D]  row t = [c_kv ; keys] of position start_pos[b] + t; a row whose
+ *               page is out of range sets MLA_DEVERR_BOUNDS and is left as it was
+ *
+ * mla_decode_attn_q8 - mla_decode_attn over the 8-bit cache: the same arguments, plan and
+ * workspace (mla_decode_workspace_size), for one query token, a few drafted ones or a whole
+ * chunk. It gives the bits that mla_decode_attn gives over a bf16 cache of the rows that
+ * mla_cache_read_q8 returns.
+ */
+int64_t mla_q8_page_bytes(const mla_dims* dims);
+mla_status mla_cache_append_q8(const mla_dims* dims, const void* c_kv, const void* k_r,
+                               const float* rope_cos, const float* rope_sin,
+                               const int32_t* block_table, int32_t max_pages_per_seq,
+                               const int32_t* start_pos, const int32_t* new_lens, int32_t batch,
+                               int32_t n_new, void* cache, int64_t num_pages, int32_t* dev_error,
+                               void* stream);
+mla_status mla_cache_read_q8(const mla_dims* dims, const void* cache, int64_t num_pages,
+                             const int32_t* block_table, int32_t max_pages_per_seq,
+                             const int32_t* start_pos, const int32_t* read_lens, int32_t batch,
+                             int32_t n, void* out, int32_t* dev_error, void* stream);
+mla_status mla_decode_attn_q8(const mla_dims* dims, const void* q_ext, const void* cache,
+                              int64_t num_pages, const int32_t* block_table,
+                              int32_t max_pages_per_seq, const int32_t* seq_lens, int32_t batch,
+                              int32_t q_len, int32_t max_seq_len, int32_t causal,
+                              int32_t num_splits, void* workspace, size_t workspace_bytes,
+                              void* o_latent, float* lse, void* stream);
+
+/*
  * mla_decode_step - one whole decode step in one call: mla_cache_append, mla_absorb_q,
  * mla_decode_attn and mla_out_up on the same arguments, in that order (the absorbed
  * order of the DeepSeek-V2 page's "Matrix absorption" section, einsums (4) and (5)).
