@@ -138,11 +138,6 @@ __global__ void __launch_bounds__(256) cache_read_q8_kernel(ReadQ8Params p) {
     const uint32_t s = ((k < 4 ? sc.x : sc.y) >> (8 * (k & 3))) & 0xFFu;
     uint32_t v[8];
     q8_decode16(codes[k], q8_factor(s), v);
-    if (s > kQ8OneFactorMax) {
-      const uint32_t f2 = q8_factor2(s);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = mul_bf16x2(v[i], f2);
-    }
     uint4* dst = reinterpret_cast<uint4*>(row + k * kQ8Cols + 16 * part);
     dst[0] = make_uint4(v[0], v[1], v[2], v[3]);
     dst[1] = make_uint4(v[4], v[5], v[6], v[7]);

@@ -34,9 +34,9 @@
 #include <algorithm>
 
 #include "decode_sched.cuh"
+#include "dequant.cuh"
 #include "kernels.h"
 #include "ptx.cuh"
-#include "q8.cuh"
 
 namespace mla {
 
@@ -60,13 +60,21 @@ __device__ unsigned long long g_mla_trace[10 * kTraceTiles + 1];
 namespace {
 
 constexpr int kThreads = 224;
-// Warps that dequantise pages of the 8-bit cache (Q8 only). Eight give each of them one 8-token
-// group of a page; with 64 query columns the softmax warps need the registers, so four take
-// two groups each.
-template <int NCOL>
-constexpr int kDequantWarps = NCOL == 64 ? 4 : 8;
-template <int NCOL, bool Q8>
-constexpr int kBlockThreads = kThreads + (Q8 ? 32 * kDequantWarps<NCOL> : 0);
+// Over the 8-bit cache (Q8) the roles are aligned groups of four warps, so that each can take
+// its own share of the registers (80 a thread at launch, 480 over the six groups): 0-2 TMA
+// producer, S^T issuer, PV issuer; 4-7 softmax and epilogue; 8-23 dequantise, two warps for
+// each 8-token group of a page, one per half of the column blocks.
+template <bool Q8>
+constexpr int kPvWarp = Q8 ? 2 : 6;
+template <bool Q8>
+constexpr int kSmWarp0 = Q8 ? 4 : 2;                 // first of the four softmax warps
+constexpr int kDqWarp0 = 8, kDqWarps = 16;
+constexpr int kRegsLaunch = 80, kRegsIssue = 40, kRegsSoftmax = 216, kRegsDequant = 56;
+static_assert(kRegsIssue + kRegsSoftmax + (kDqWarps / 4) * kRegsDequant <=
+                  (2 + kDqWarps / 4) * kRegsLaunch,
+              "the groups' registers exceed what the block is launched with");
+template <bool Q8>
+constexpr int kBlockThreads = Q8 ? 32 * (kDqWarp0 + kDqWarps) : kThreads;
 constexpr int kBlkBytes = kDecodeTok * 128;   // one 64 x 64 bf16 block, 8 KB
 constexpr float kLazyThreshold = 8.0f;        // log2 units
 // Initial reference max: finite, so a masked score (-inf) minus it is exactly -inf (weight
@@ -170,7 +178,7 @@ size_t decode_smem_bytes(int ncol, int nblk, int slot_blocks, int nslot, int npt
 }
 
 template <int NCOL, bool Q8>
-__global__ void __launch_bounds__(kBlockThreads<NCOL, Q8>, 1)
+__global__ void __launch_bounds__(kBlockThreads<Q8>, 1)
     mla_decode_kernel(const __grid_constant__ DecodeParams p) {
   constexpr int HALF = NCOL / 2;
   extern __shared__ uint8_t smem_raw[];
@@ -216,7 +224,7 @@ __global__ void __launch_bounds__(kBlockThreads<NCOL, Q8>, 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < p.nslot; ++s) {
-      mbar_init(&full[s], Q8 ? 1 + kDequantWarps<NCOL> : 1);
+      mbar_init(&full[s], Q8 ? 1 + kDqWarps : 1);
       mbar_init(&empty[s], 1);
     }
     mbar_init(q_full, 1);
@@ -241,7 +249,7 @@ __global__ void __launch_bounds__(kBlockThreads<NCOL, Q8>, 1)
   // ---- schedule: this CTA's tile range [r0, r1) in its row block, first sequence -------
   // The row blocks of a sequence are worked on in lockstep by neighbouring CTAs, so the
   // second read of every page is served from L2.
-  find_tile_range<kBlockThreads<NCOL, Q8>>(p, vc, vgrid, blockIdx.x == 0, warp_sum, sched);
+  find_tile_range<kBlockThreads<Q8>>(p, vc, vgrid, blockIdx.x == 0, warp_sum, sched);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -249,6 +257,9 @@ __global__ void __launch_bounds__(kBlockThreads<NCOL, Q8>, 1)
   const int r0 = sched[2], r1 = sched[3], per = sched[4];
   const bool has_work = sched[0] >= 0 && r0 < r1;
 
+  const bool issuer = Q8 ? warp < 4 : warp < 2 || warp == kPvWarp<Q8>;
+  if (issuer) {
+  if constexpr (Q8) reg_dec<kRegsIssue>();
   if (warp == 0) {
     // ===================================== TMA producer ==================================
     if (has_work && elect_one()) {
@@ -259,6 +270,8 @@ __global__ void __launch_bounds__(kBlockThreads<NCOL, Q8>, 1)
       int jj = 0, pc = 0;
       SlotRing ring(p.nslot);
       bool ok = true;
+      PageWalk ahead{w};                  // the page to bring into L2 next (Q8 only)
+      if constexpr (Q8) ahead = PageWalk(p, cg, r0, sched[0], sched[1]);
       for (; ok && w.s < r1; w.s += w.tiles, ++w.b, ++pc) {
         w.load(p, cg);
         p.unit_start[w.u] = w.s;   // same value from every CTA that touches the unit
@@ -272,6 +285,7 @@ __global__ void __launch_bounds__(kBlockThreads<NCOL, Q8>, 1)
           const int slot = ring.slot;
           // the page id is read before the wait, so its round trip overlaps it
           int32_t page = bt[t - w.s];
+          if constexpr (Q8) prefetch_pages(p, cg, r1, t + kDequantPrefetch, ahead);
           if (jj >= p.nslot && !mbar_wait(&empty[slot], (ring.round - 1) & 1, wc)) {
             ok = false;
             break;
@@ -327,6 +341,7 @@ __global__ void __launch_bounds__(kBlockThreads<NCOL, Q8>, 1)
           tc_fence_after();
           const uint32_t soff = slot * slot_bytes;
           if (!mbar_wait(&full[slot], ring.round & 1, wc)) { ok = false; break; }
+          if (Q8) fence_proxy_async_smem();   // the dequantising warps' stores, to the UMMAs
           tc_fence_after();
           MLA_TRACE_AT(9, jj);
           // K steps of 16 columns over the row width; the descriptors step 32 bytes within
@@ -350,7 +365,7 @@ __global__ void __launch_bounds__(kBlockThreads<NCOL, Q8>, 1)
       }
     }
     __syncwarp();
-  } else if (warp == 6) {
+  } else if (warp == kPvWarp<Q8>) {
     // =============================== UMMA issuer for PV ==================================
     // O^T += C^T P^T for page j once the four softmax warps have written P^T(j) and zeroed
     // the page's rows past the context; the first page of a piece overwrites O^T (the
@@ -396,88 +411,23 @@ __global__ void __launch_bounds__(kBlockThreads<NCOL, Q8>, 1)
       }
     }
     __syncwarp();
-  } else if (Q8 && warp >= 7) {
+  }
+  } else if (Q8 && warp >= kDqWarp0) {
     // ============================== dequantising warps (Q8) ==============================
-    // Each 8-token group of a page is one warp's (lane: token lane / 4, 16 of the 64 columns
-    // of every block). The next page's codes are loaded into registers as this page's leave
-    // them, so a whole page per CTA is always on its way from memory without shared memory to
-    // hold it, and the page takes no trip through shared memory as codes.
+    if constexpr (Q8) reg_dec<kRegsDequant>();
     if (has_work) {
-      constexpr int NG = 8 / kDequantWarps<NCOL>;       // 8-token groups of this warp
-      const int lb = p.r / kQ8Cols;
-      const int part = lane & 3;
-      const int64_t page_bytes = q8_page_bytes(p.r, p.D - p.r);
-      const int sc_off = q8_scales_offset(p.r, p.D - p.r);
-      uint4 codes[NG][kQ8MaxBlocks];
-      uint2 scales[NG];
-      UnitWalk w{sched[0], sched[1]};
-      w.load(p, cg);
-      int t = r0;
-      // codes and scales of this warp's tokens in tile t; zero codes past the context, whose
-      // rows must not reach O^T (0-weight x garbage)
-      auto fetch = [&]() {
-        int32_t page = p.block_table[int64_t(w.b) * p.max_pages + (t - w.s)];
-        if (page < 0 || page >= p.num_pages) page = 0;   // the producer reports it
-        const uint8_t* src = static_cast<const uint8_t*>(p.cache_q8) + page * page_bytes;
-#pragma unroll
-        for (int g = 0; g < NG; ++g) {
-          const int tok = 8 * ((warp - 7) * NG + g) + (lane >> 2);
-          const bool live = (t - w.s) * kDecodeTok + tok < w.L;
-          scales[g] = live ? *reinterpret_cast<const uint2*>(src + sc_off + tok * kQ8ScaleBytes)
-                           : make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
-#pragma unroll
-          for (int k = 0; k < kQ8MaxBlocks; ++k)
-            codes[g][k] = (k < lb && live) ? ld_stream_v4(src + k * kQ8BlockBytes + tok * kQ8Cols +
-                                                          16 * part)
-                                           : make_uint4(0, 0, 0, 0);
-        }
-      };
-      fetch();
-      SlotRing ring(p.nslot);
-      for (int jj = 0;; ++jj, ring.next()) {
-        if (jj >= p.nslot &&
-            !__all_sync(0xffffffffu, mbar_wait(&empty[ring.slot], (ring.round - 1) & 1, wc)))
-          break;
-        uint8_t* sbase = slots + ring.slot * slot_bytes;
-#pragma unroll
-        for (int g = 0; g < NG; ++g) {
-          const int tok = 8 * ((warp - 7) * NG + g) + (lane >> 2);
-          uint8_t* rowp = sbase + tok * 128;
-#pragma unroll
-          for (int k = 0; k < kQ8MaxBlocks; ++k) {
-            if (k >= lb) break;
-            const uint32_t s = ((k < 4 ? scales[g].x : scales[g].y) >> (8 * (k & 3))) & 0xFFu;
-            uint32_t v[8];
-            q8_decode16(codes[g][k], q8_factor(s), v);
-            if (s > kQ8OneFactorMax) {
-              const uint32_t f2 = q8_factor2(s);
-#pragma unroll
-              for (int i = 0; i < 8; ++i) v[i] = mul_bf16x2(v[i], f2);
-            }
-            uint8_t* blk = rowp + k * kBlkBytes;
-            *reinterpret_cast<uint4*>(blk + (((2 * part) ^ (tok & 7)) << 4)) =
-                make_uint4(v[0], v[1], v[2], v[3]);
-            *reinterpret_cast<uint4*>(blk + (((2 * part + 1) ^ (tok & 7)) << 4)) =
-                make_uint4(v[4], v[5], v[6], v[7]);
-          }
-        }
-        if (++t == w.s + w.tiles) {                      // on to the next unit
-          w.s += w.tiles;
-          ++w.b;
-          if (t < r1) w.load(p, cg);
-        }
-        if (t < r1) fetch();
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&full[ring.slot]);
-        if (t >= r1) break;
-      }
+      const int wi = warp - kDqWarp0, lb = p.r / kQ8Cols;
+      const int half = (lb + 1) / 2, blk0 = wi < 8 ? 0 : half;
+      dequant_pages(p, cg, r0, r1, sched[0], sched[1], wi & 7, blk0, wi < 8 ? half : lb - half,
+                    blk0, slots, slot_bytes, full, empty, wc);
     }
-  } else if (has_work) {   // warps 2-5
+  } else {
+  if constexpr (Q8) reg_inc<kRegsSoftmax>();
+  if (has_work) {
     // ================================ softmax, epilogue ==================================
     const int sp = warp & 3;                  // TMEM sub-partition this warp may access
-    const int wi = warp - 2;                  // index among the 4 softmax warps
-    const int tid = threadIdx.x - 64;         // 0..127
+    const int wi = (sp + 2) & 3;              // index among the 4 softmax warps
+    const int tid = threadIdx.x - 32 * kSmWarp0<Q8>;   // 0..127
     const uint32_t lane_base = uint32_t(sp * 32) << 16;
     const int tok = 16 * sp + (lane & 15);    // token of this thread inside the tile
     const int hf = lane >> 4;                 // which half of the columns
@@ -503,7 +453,7 @@ __global__ void __launch_bounds__(kBlockThreads<NCOL, Q8>, 1)
         const int sb = jj & 1;
         const uint32_t s_addr = tmem + lane_base + sb * NCOL;
         const bool got = __all_sync(0xffffffffu, mbar_wait(&s_full[sb], (jj >> 1) & 1, wc));
-        if (threadIdx.x == 64) MLA_TRACE_AT(4, jj);
+        if (tid == 0) MLA_TRACE_AT(4, jj);
         const int tile_pos0 = (t - w.s) * kDecodeTok;
         const int pos = tile_pos0 + tok;
         const bool ragged = !got || tile_pos0 + kDecodeTok - 1 > last_full;
@@ -532,7 +482,7 @@ __global__ void __launch_bounds__(kBlockThreads<NCOL, Q8>, 1)
         const bool exceed = __any_sync(0xffffffffu, tmax > kLazyThreshold);
         if (lane == 0) flags[(jj & 1) * 4 + wi] = exceed ? 1 : 0;
         named_bar_sync(1, 128);
-        if (threadIdx.x == 64) MLA_TRACE_AT(5, jj);
+        if (tid == 0) MLA_TRACE_AT(5, jj);
         const int* fl = flags + (jj & 1) * 4;
         if ((fl[0] | fl[1] | fl[2] | fl[3]) != 0) {
           // Move the reference to the running column max of the scaled scores; the raw
@@ -605,7 +555,7 @@ __global__ void __launch_bounds__(kBlockThreads<NCOL, Q8>, 1)
 
         // unnormalised weights p = 2^(s*c - m) into this tile's P^T buffer (bf16)
         if (jj >= p.npt) mbar_wait(&pv_done[(jj - p.npt) & 1], ((jj - p.npt) >> 1) & 1, wc);
-        if (threadIdx.x == 64) MLA_TRACE_AT(6, jj);
+        if (tid == 0) MLA_TRACE_AT(6, jj);
         uint32_t packed[HALF / 2];
 #pragma unroll
         for (int j = 0; j < HALF; j += 2) {
@@ -716,6 +666,7 @@ __global__ void __launch_bounds__(kBlockThreads<NCOL, Q8>, 1)
       tc_fence_before();
     }
   }
+  }
 
   tc_fence_before();
   __syncthreads();
@@ -736,7 +687,7 @@ static cudaError_t launch_decode_n(const DecodeParams& p, dim3 grid, size_t smem
   cudaError_t e = cudaFuncSetAttribute(mla_decode_kernel<NCOL, Q8>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
   if (e != cudaSuccess) return e;
-  return launch_pdl(mla_decode_kernel<NCOL, Q8>, grid, dim3(kBlockThreads<NCOL, Q8>), smem, stream,
+  return launch_pdl(mla_decode_kernel<NCOL, Q8>, grid, dim3(kBlockThreads<Q8>), smem, stream,
                     1, p);
 }
 

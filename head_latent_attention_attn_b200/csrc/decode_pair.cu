@@ -39,9 +39,9 @@
 #include <math.h>
 
 #include "decode_sched.cuh"
+#include "dequant.cuh"
 #include "kernels.h"
 #include "ptx.cuh"
-#include "q8.cuh"
 
 namespace mla {
 
@@ -69,14 +69,20 @@ __device__ unsigned long long g_mla_pair_trace[kPairTraceEvents * kPairTraceTile
 namespace {
 
 constexpr int kPvWarp = 2;
-// First of the 12 row warps. Over the 8-bit cache (Q8) four more warps follow them, which
-// dequantise this CTA's half of each page, and the row warps start at 4 so that every role is
-// one aligned group of four warps and can take its own share of the registers.
+// First of the 12 row warps. Over the 8-bit cache (Q8) eight more warps follow them, which
+// dequantise this CTA's half of each page, one per 8-token group, and the row warps start at 4
+// so that every role is an aligned group of four warps and can take its own share of the
+// registers (80 a thread at launch, 480 over the six groups).
 template <bool Q8>
 constexpr int kRowWarp0 = Q8 ? 4 : 3;
+constexpr int kDqWarp0 = kRowWarp0<true> + 12, kDqWarps = 8;
 template <bool Q8>
-constexpr int kThreads = 32 * (kRowWarp0<Q8> + 12 + (Q8 ? 4 : 0));
-constexpr int kDequantWarp0 = kRowWarp0<true> + 12;
+constexpr int kThreads = 32 * (Q8 ? kDqWarp0 + kDqWarps : kRowWarp0<Q8> + 12);
+constexpr int kRegsLaunch = 80, kRegsIssue = 40, kRegsOwner = 128, kRegsSender = 96,
+              kRegsReceiver = 96, kRegsDequant = 56;
+static_assert(kRegsIssue + kRegsOwner + kRegsSender + kRegsReceiver +
+                      (kDqWarps / 4) * kRegsDequant <= (4 + kDqWarps / 4) * kRegsLaunch,
+              "the groups' registers exceed what the block is launched with");
 constexpr int kHalfTok = kDecodeTok / 2;                       // tokens per owner thread
 constexpr uint32_t kBlk = kDecodeTok * 128;                    // 64 x 64 bf16 block, 8 KB
 constexpr int kPackWords = kHalfTok * 3 / 4;                   // 24-bit values of a half row
@@ -294,7 +300,7 @@ __global__ void __launch_bounds__(kThreads<Q8>, 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < p.nslot; ++s) {
-      mbar_init(&full[s], Q8 ? 1 + 4 : 1);             // the TMA producer, 4 dequantising warps
+      mbar_init(&full[s], Q8 ? 1 + kDqWarps : 1);
       mbar_init(&empty[s], 1);
     }
     mbar_init(q_full, 8);                              // 4 owner + 4 sender warps
@@ -337,6 +343,9 @@ __global__ void __launch_bounds__(kThreads<Q8>, 1)
     g_mla_pair_trace[kPairTraceEvents * kPairTraceTiles + 2 * blockIdx.x] = globaltimer_ns();
 #endif
 
+  const bool issuer = warp < kRowWarp0<Q8>;
+  if (issuer) {
+  if constexpr (Q8) reg_dec<kRegsIssue>();
   if (warp == 0) {
     // ===================================== TMA producer ==================================
     if (has_work && elect_one()) {
@@ -411,6 +420,7 @@ __global__ void __launch_bounds__(kThreads<Q8>, 1)
           const int sb = jj & 1;
           // every block of the tile landed, then the S buffer free
           if (!mbar_wait(&full[slot], ring.round & 1, wc)) { ok = false; break; }
+          if (Q8) fence_proxy_async_smem();   // the dequantising warps' stores, to the UMMAs
           MLA_PTRACE(1, jj);
           if (jj >= 2 && !mbar_wait(&s_free[sb], ((jj - 2) >> 1) & 1, wc)) {
             ok = false;
@@ -478,83 +488,13 @@ __global__ void __launch_bounds__(kThreads<Q8>, 1)
       }
     }
     __syncwarp();
-  } else if (Q8 && warp >= kDequantWarp0) {
+  }
+  } else if (Q8 && warp >= kDqWarp0) {
     // ============================== dequantising warps (Q8) ==============================
-    // This CTA's r/2 latent columns of each page, as in the one-CTA kernel (decode.cu): two
-    // 8-token groups a warp, the next page's codes loaded as this page's leave the registers.
-    if (has_work) {
-      constexpr int NG = 2;
-      constexpr int kHalfBlocks = kQ8MaxBlocks / 2;
-      const int part = lane & 3;
-      const int64_t page_bytes = q8_page_bytes(r, p.D - r);
-      const int sc_off = q8_scales_offset(r, p.D - r);
-      uint4 codes[NG][kHalfBlocks];
-      uint32_t scales[NG];                               // of this CTA's blocks, a byte each
-      UnitWalk w{sched[0], sched[1]};
-      w.load(p, cg);
-      int t = r0;
-      auto fetch = [&]() {
-        int32_t page = p.block_table[int64_t(w.b) * p.max_pages + (t - w.s)];
-        if (page < 0 || page >= p.num_pages) page = 0;   // the producer reports it
-        const uint8_t* src = static_cast<const uint8_t*>(p.cache_q8) + page * page_bytes;
-#pragma unroll
-        for (int g = 0; g < NG; ++g) {
-          const int tok = 8 * ((warp - kDequantWarp0) * NG + g) + (lane >> 2);
-          const bool live = (t - w.s) * kDecodeTok + tok < w.L;
-          uint2 sc = make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
-          if (live) sc = *reinterpret_cast<const uint2*>(src + sc_off + tok * kQ8ScaleBytes);
-          scales[g] = uint32_t((uint64_t(sc.y) << 32 | sc.x) >> (8 * lb * int(rank)));
-#pragma unroll
-          for (int k = 0; k < kHalfBlocks; ++k)
-            codes[g][k] = (k < lb && live)
-                              ? ld_stream_v4(src + (int(rank) * lb + k) * kQ8BlockBytes +
-                                             tok * kQ8Cols + 16 * part)
-                              : make_uint4(0, 0, 0, 0);
-        }
-      };
-      fetch();
-      SlotRing ring(p.nslot);
-      for (int jj = 0;; ++jj, ring.next()) {
-        if (jj >= p.nslot &&
-            !__all_sync(0xffffffffu, mbar_wait(&empty[ring.slot], (ring.round - 1) & 1, wc)))
-          break;
-        uint8_t* sbase = slots + ring.slot * lay.slot_bytes;
-#pragma unroll
-        for (int g = 0; g < NG; ++g) {
-          const int tok = 8 * ((warp - kDequantWarp0) * NG + g) + (lane >> 2);
-          uint8_t* rowp = sbase + tok * 128;
-#pragma unroll
-          for (int k = 0; k < kHalfBlocks; ++k) {
-            if (k >= lb) break;
-            const uint32_t s = (scales[g] >> (8 * k)) & 0xFFu;
-            uint32_t v[8];
-            q8_decode16(codes[g][k], q8_factor(s), v);
-            if (s > kQ8OneFactorMax) {
-              const uint32_t f2 = q8_factor2(s);
-#pragma unroll
-              for (int i = 0; i < 8; ++i) v[i] = mul_bf16x2(v[i], f2);
-            }
-            uint8_t* blk = rowp + k * kBlk;
-            *reinterpret_cast<uint4*>(blk + (((2 * part) ^ (tok & 7)) << 4)) =
-                make_uint4(v[0], v[1], v[2], v[3]);
-            *reinterpret_cast<uint4*>(blk + (((2 * part + 1) ^ (tok & 7)) << 4)) =
-                make_uint4(v[4], v[5], v[6], v[7]);
-          }
-        }
-        if (++t == w.s + w.tiles) {                      // on to the next unit
-          w.s += w.tiles;
-          ++w.b;
-          if (t < r1) w.load(p, cg);
-        }
-        if (t < r1) fetch();
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&full[ring.slot]);
-        if (t >= r1) break;
-      }
-    }
-  } else if (Q8 && warp == 3) {
-    // spare: fills the issuers' group of four warps
+    if constexpr (Q8) reg_dec<kRegsDequant>();
+    if (has_work)
+      dequant_pages(p, cg, r0, r1, sched[0], sched[1], warp - kDqWarp0, int(rank) * lb, lb, 0,
+                    slots, lay.slot_bytes, full, empty, wc);
   } else if (has_work) {
     // ==================================== the 128 rows ====================================
     // Every row warp works on 16 TMEM lanes of its sub-partition with 16x32bx2 accesses:
@@ -687,6 +627,7 @@ __global__ void __launch_bounds__(kThreads<Q8>, 1)
     };
 
     if (role == 0) {
+      if constexpr (Q8) reg_inc<kRegsOwner>();
       // ------------- owner: this CTA's 16 rows of sub-partition sp; softmax and P ---------
       const int qi = row / p.num_heads;
       load_q(sched[0]);
@@ -840,6 +781,7 @@ __global__ void __launch_bounds__(kThreads<Q8>, 1)
         w.load(p, cg);
       }
     } else if (role == 1) {
+      if constexpr (Q8) reg_inc<kRegsSender>();
       // ------------- sender: the partner's 16 rows of sub-partition sp, partial scores ----
       load_q(sched[0]);
       UnitWalk w{sched[0], sched[1]};
@@ -884,6 +826,7 @@ __global__ void __launch_bounds__(kThreads<Q8>, 1)
         }
       }
     } else {
+      if constexpr (Q8) reg_inc<kRegsReceiver>();
       // ------------- receiver: the partner's weights for its 16 rows of sub-partition sp --
       UnitWalk w{sched[0], sched[1]};
       w.load(p, cg);

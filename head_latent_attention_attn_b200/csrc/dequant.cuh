@@ -1,0 +1,131 @@
+// dequant.cuh - the part of the decode kernels that turns pages of the 8-bit cache (q8.cuh)
+// into the bf16 tiles that the UMMAs read.
+//
+// A page's codes go from memory to the registers of the dequantising warps and from there, as
+// bf16, into the cache slot: no shared memory holds them in between, which the largest shapes
+// do not have. A warp converts 8 tokens (lane: token lane / 4, 16 of the 64 columns) of up to
+// four column blocks; its loads of the next page are issued as soon as this page's codes have
+// left the registers, and the TMA producer brings pages into L2 ahead of them.
+#pragma once
+
+#include "decode_sched.cuh"
+#include "q8.cuh"
+
+namespace mla {
+
+constexpr uint32_t kBlk8Bytes = kDecodeTok * 128;   // one 64 x 64 bf16 block of a slot
+constexpr int kDequantBlocks = 4;                   // column blocks of a warp at most
+constexpr int kDequantPrefetch = 3;                 // pages that the L2 prefetch runs ahead
+
+MLA_DEVICE void st_shared_v4(uint32_t saddr, const uint32_t* v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(saddr), "r"(v[0]), "r"(v[1]),
+               "r"(v[2]), "r"(v[3])
+               : "memory");
+}
+
+// `bytes` (a multiple of 16) at p, 16-byte aligned, into L2.
+MLA_DEVICE void prefetch_l2(const void* p, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
+}
+
+// Tile by tile along [r0, r1): the page of each, its first position and its context length.
+struct PageWalk {
+  UnitWalk w;
+  int t;
+  MLA_DEVICE explicit PageWalk(const UnitWalk& u) : w(u), t(0) {}
+  MLA_DEVICE PageWalk(const DecodeParams& p, int cg, int r0, int b, int s) : w{b, s}, t(r0) {
+    w.load(p, cg);
+  }
+  MLA_DEVICE int32_t page(const DecodeParams& p) const {
+    return p.block_table[int64_t(w.b) * p.max_pages + (t - w.s)];
+  }
+  // to the next tile; the caller stops at r1
+  MLA_DEVICE void next(const DecodeParams& p, int cg, int r1) {
+    if (++t == w.s + w.tiles && t < r1) {
+      w.s += w.tiles;
+      ++w.b;
+      w.load(p, cg);
+    }
+  }
+};
+
+// Bring the pages of the tiles up to `upto` (exclusive of r1) into L2; one thread.
+MLA_DEVICE void prefetch_pages(const DecodeParams& p, int cg, int r1, int upto, PageWalk& ahead) {
+  const int64_t page_bytes = q8_page_bytes(p.r, p.D - p.r);
+  while (ahead.t < r1 && ahead.t <= upto) {
+    const int32_t page = ahead.page(p);
+    if (page >= 0 && page < p.num_pages)
+      prefetch_l2(static_cast<const uint8_t*>(p.cache_q8) + page * page_bytes,
+                  uint32_t(page_bytes));
+    ahead.next(p, cg, r1);
+  }
+}
+
+// All pages of tiles [r0, r1), whose first is of sequence b, which starts at tile s. This warp
+// converts 8-token group `grp` of the page's column blocks [blk0, blk0 + nb), nb <= 4 (0: it
+// only takes part in the slots' hand-over), into the slot's blocks dst0, dst0 + 1, ... It waits
+// for empty[slot] and arrives once on full[slot].
+MLA_DEVICE void dequant_pages(const DecodeParams& p, int cg, int r0, int r1, int b, int s, int grp,
+                              int blk0, int nb, int dst0, uint8_t* slots, uint32_t slot_bytes,
+                              uint64_t* full, uint64_t* empty, const WaitCtx& wc) {
+  const int lane = threadIdx.x & 31, part = lane & 3;
+  const int tok = 8 * grp + (lane >> 2);
+  const int R = p.D - p.r;
+  const int64_t page_bytes = q8_page_bytes(p.r, R);
+  const uint8_t* codes_at = static_cast<const uint8_t*>(p.cache_q8) + blk0 * kQ8BlockBytes +
+                            tok * kQ8Cols + 16 * part;
+  const uint8_t* scale_at =
+      static_cast<const uint8_t*>(p.cache_q8) + q8_scales_offset(p.r, R) + tok * kQ8ScaleBytes;
+  const uint32_t st0 = smem_u32(slots) + dst0 * kBlk8Bytes + tok * 128 +
+                       (((2 * part) ^ (tok & 7)) << 4);
+
+  PageWalk next(p, cg, r0, b, s);        // the tile to fetch; its page id is read a tile ahead
+  int32_t page = next.page(p);
+  uint4 codes[kDequantBlocks];
+  uint2 scales;
+  uint32_t live;                         // zero for a token past the context, else all ones
+  auto fetch = [&]() {
+    if (page < 0 || page >= p.num_pages) page = 0;       // the TMA producer reports it
+    const int64_t off = page * page_bytes;
+    live = (next.t - next.w.s) * kDecodeTok + tok < next.w.L ? ~0u : 0u;
+#pragma unroll
+    for (int k = 0; k < kDequantBlocks; ++k)
+      if (k < nb) codes[k] = ld_stream_v4(codes_at + off + k * kQ8BlockBytes);
+    scales = *reinterpret_cast<const uint2*>(scale_at + off);
+    next.next(p, cg, r1);
+    if (next.t < r1) page = next.page(p);
+  };
+
+  fetch();
+  SlotRing ring(p.nslot);
+  for (int jj = 0, n = r1 - r0; jj < n; ++jj, ring.next()) {
+    if (jj >= p.nslot &&
+        !__all_sync(0xffffffffu, mbar_wait(&empty[ring.slot], (ring.round - 1) & 1, wc)))
+      break;
+    const uint32_t at = st0 + ring.slot * slot_bytes;
+    uint32_t sc = uint32_t((uint64_t(scales.y) << 32 | scales.x) >> (8 * blk0));
+    if (__any_sync(0xffffffffu, live == 0)) {
+      // the context ends in this group: the rows past it, which may hold anything, become zeros
+      // (0-weight x garbage must not reach O)
+      sc &= live;
+#pragma unroll
+      for (int k = 0; k < kDequantBlocks; ++k)
+        codes[k] = make_uint4(codes[k].x & live, codes[k].y & live, codes[k].z & live,
+                              codes[k].w & live);
+    }
+#pragma unroll
+    for (int k = 0; k < kDequantBlocks; ++k) {
+      if (k >= nb) break;
+      uint32_t v[8];
+      q8_decode16(codes[k], q8_factor((sc >> (8 * k)) & 0xFFu), v);
+      st_shared_v4(at + k * kBlk8Bytes, v);
+      st_shared_v4((at ^ 16u) + k * kBlk8Bytes, v + 4);
+    }
+    // no proxy fence here: the UMMA issuer fences after it has waited for full[slot]
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&full[ring.slot]);
+    if (next.t < r1) fetch();
+  }
+}
+
+}  // namespace mla

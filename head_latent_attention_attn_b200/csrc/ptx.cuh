@@ -37,6 +37,17 @@ MLA_DEVICE bool elect_one() {
   return pred != 0;
 }
 
+// Give back registers down to N a thread, or take up to N (which waits until the block has
+// them free): executed by all four warps of an aligned group.
+template <int N>
+MLA_DEVICE void reg_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+MLA_DEVICE void reg_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
 MLA_DEVICE void named_bar_sync(uint32_t id, uint32_t nthreads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
 }
