@@ -38,7 +38,7 @@ C_SYMBOLS = ("mla_row_width", "mla_status_string", "mla_cache_append", "mla_abso
              "mla_kv_shared_decode_dims", "mla_kv_shared_query", "mla_kv_shared_output",
              "mla_down_kv_append", "mla_out_proj_workspace_size",
              "mla_out_proj", "mla_decode_step", "mla_q8_page_bytes", "mla_cache_append_q8",
-             "mla_cache_read_q8", "mla_decode_attn_q8")
+             "mla_cache_read_q8", "mla_decode_attn_q8", "mla_prefill_attn")
 
 
 class MlaError(RuntimeError):
@@ -128,6 +128,9 @@ def lib() -> ctypes.CDLL:
     L.mla_cache_read_q8.restype = _I32
     L.mla_decode_attn_q8.argtypes = L.mla_decode_attn.argtypes
     L.mla_decode_attn_q8.restype = _I32
+    L.mla_prefill_attn.argtypes = [D, _P, _P, _I64, _I64, _P, _I64, _P, _I64, _I64, _P, _P, _I32,
+                                   _I32, _I32, _I32, _P, _P, _P, _P]
+    L.mla_prefill_attn.restype = _I32
     _lib = L
     return L
 
@@ -441,6 +444,65 @@ def mla_decode_attn_q8(dims: MlaDims, q_ext, cache, block_table, seq_lens, max_s
     _check(st, "mla_decode_attn_q8")
 
 
+def _per_token(t, name: str, shape):
+    """Token and head strides of a bf16 CUDA tensor [B, n, heads, width] whose last dim is
+    contiguous and whose batches follow one another. (The stride of a dim of size 1 says nothing.)"""
+    if not isinstance(t, torch.Tensor) or t.device.type != "cuda" or t.dtype != torch.bfloat16:
+        raise MlaError(f"{name} must be a bfloat16 CUDA tensor", MLA_ERR_INVALID_ARG)
+    if tuple(t.shape) != tuple(shape):
+        raise MlaError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}",
+                       MLA_ERR_INVALID_ARG)
+    B, n, heads, width = shape
+    sb, st, sh, sw = t.stride()
+    if heads == 1:
+        sh = width
+    if n == 1:
+        st = sb if B > 1 else heads * sh
+    if sw != 1 or (B > 1 and sb != n * st):
+        raise MlaError(f"{name} has strides {t.stride()}: the last dim must be contiguous and a "
+                       "batch must be n tokens", MLA_ERR_INVALID_ARG)
+    return st, sh
+
+
+def mla_prefill_attn(dims: MlaDims, q, k_nope, k_pe, v, seq_lens, o, lse, q_lens=None,
+                     causal: bool = True, dev_error=None, stream=None) -> None:
+    """Attention in its expanded form: q [B, q, H, d_n + d_r] (rotated), k_nope [B, n, H, d_n],
+    k_pe [B, n, G, d_r] (rotated, one per group) and v [B, n, H, d_v] give o [B, q, H, d_v]
+    (bf16) and lse [B, q, H] (fp32). Row i of sequence b is at position
+    seq_lens[b] - q_lens[b] + i (q_lens None: all q rows); k_nope, k_pe and v may be views with
+    token and head strides (the halves of a packed projection, columns of cache rows)."""
+    if not isinstance(q, torch.Tensor) or q.dim() != 4:
+        raise MlaError("q must be a tensor [B, q, H, d_n + d_r]", MLA_ERR_INVALID_ARG)
+    if not isinstance(k_nope, torch.Tensor) or k_nope.dim() != 4:
+        raise MlaError("k_nope must be a tensor [B, n, H, d_n]", MLA_ERR_INVALID_ARG)
+    B, ql, n = q.shape[0], q.shape[1], k_nope.shape[1]
+    H, G, dn, dr, dv = (dims.num_heads, dims.num_kv_groups, dims.qk_nope_dim, dims.rope_dim,
+                        dims.v_head_dim)
+    _need(q, "q", torch.bfloat16, (B, ql, H, dn + dr))
+    k_tok, k_head = _per_token(k_nope, "k_nope", (B, n, H, dn))
+    v_tok, v_head = _per_token(v, "v", (B, n, H, dv))
+    kr_tok = 0
+    if dr > 0:
+        kr_tok, kr_group = _per_token(k_pe, "k_pe", (B, n, G, dr))
+        if kr_group != dr:
+            raise MlaError("the groups of k_pe must follow one another", MLA_ERR_INVALID_ARG)
+    else:
+        k_pe = None
+    _need(seq_lens, "seq_lens", torch.int32, (B,))
+    _need(o, "o", torch.bfloat16, (B, ql, H, dv))
+    _need(lse, "lse", torch.float32, (B, ql, H))
+    if q_lens is not None:
+        _need(q_lens, "q_lens", torch.int32, (B,))
+    if dev_error is not None:
+        _need(dev_error, "dev_error", torch.int32)
+    with _one_device((q, k_nope, k_pe, v, seq_lens, o, lse, q_lens, dev_error), stream):
+        st = lib().mla_prefill_attn(
+            ctypes.byref(dims), _ptr(q), _ptr(k_nope), k_tok, k_head, _ptr(k_pe), kr_tok, _ptr(v),
+            v_tok, v_head, _ptr(seq_lens), _ptr(q_lens), B, ql, n, 1 if causal else 0, _ptr(o),
+            _ptr(lse), _ptr(dev_error), _stream(stream))
+    _check(st, "mla_prefill_attn")
+
+
 def mla_kv_shared_decode_dims(dims: MlaDims) -> MlaDims:
     """Decode view of a K = V layout: the whole cache row is the latent (rank D, no rotary
     slot), so mla_decode_attn with these dims returns o_latent = sum_l p_l row_l."""
@@ -591,5 +653,5 @@ __all__ = ["MlaDims", "MlaError", "make_dims", "lib", "mla_row_width", "mla_cach
            "mla_kv_shared_output", "mla_down_kv_append",
            "mla_out_proj_workspace_size",
            "mla_out_proj", "mla_get_device_status", "mla_decode_step", "mla_q8_page_bytes",
-           "mla_cache_append_q8", "mla_cache_read_q8", "mla_decode_attn_q8", "C_SYMBOLS",
-           "STATUS_NAMES"]
+           "mla_cache_append_q8", "mla_cache_read_q8", "mla_decode_attn_q8", "mla_prefill_attn",
+           "C_SYMBOLS", "STATUS_NAMES"]

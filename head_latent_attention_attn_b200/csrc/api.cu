@@ -946,6 +946,71 @@ mla_status mla_kv_shared_output(const mla_dims* dims, const void* o_latent, cons
   return kv_shared_rotate(dims, o_latent, rope_cos, rope_sin, batch, q_len, o, 1, stream);
 }
 
+mla_status mla_prefill_attn(const mla_dims* dims, const void* q, const void* k_nope,
+                            int64_t k_token_stride, int64_t k_head_stride, const void* k_pe,
+                            int64_t k_pe_token_stride, const void* v, int64_t v_token_stride,
+                            int64_t v_head_stride, const int32_t* seq_lens, const int32_t* q_lens,
+                            int32_t batch, int32_t q_len, int32_t kv_len, int32_t causal, void* o,
+                            float* lse, int32_t* dev_error, void* stream) {
+  mla_status st = check_dims(dims);
+  if (st != MLA_OK) return st;
+  const int H = dims->num_heads, G = dims->num_kv_groups;
+  const int dn = dims->qk_nope_dim, dr = dims->rope_dim, dv = dims->v_head_dim;
+  if (batch < 0 || q_len <= 0 || kv_len <= 0 || (causal != 0 && causal != 1))
+    return MLA_ERR_INVALID_ARG;
+  if (dn > 128 || dv > 128 || dr > 64 || dr % 8 != 0) return MLA_ERR_UNSUPPORTED;
+  if (batch == 0) return MLA_OK;
+  if (!q || !k_nope || !v || !seq_lens || !o || !lse || (dr > 0 && !k_pe))
+    return MLA_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(k_nope, 16) || !aligned(v, 16) || !aligned(o, 16) ||
+      (dr > 0 && !aligned(k_pe, 16)))
+    return MLA_ERR_INVALID_ARG;
+  // a head's row lies inside its stride, and the heads of a token inside the token's; TMA
+  // strides are multiples of 16 bytes below 2^40
+  auto strides_ok = [&](int64_t tok, int64_t head, int width, int heads) {
+    return head >= width && tok >= head * (heads - 1) + width && head % 8 == 0 && tok % 8 == 0 &&
+           tok < (int64_t(1) << 38) / kv_len;
+  };
+  if (!strides_ok(k_token_stride, k_head_stride, dn, H) ||
+      !strides_ok(v_token_stride, v_head_stride, dv, H) ||
+      (dr > 0 && !strides_ok(k_pe_token_stride, dr, dr, G)))
+    return MLA_ERR_INVALID_ARG;
+  if (H > 65535 || batch > 65535) return MLA_ERR_UNSUPPORTED;
+  PrefillParams p{};
+  const int64_t dq = dn + dr;
+  auto map4 = [&](CUtensorMap* m, const void* at, int width, int heads, int64_t len,
+                  int64_t head_stride, int64_t token_stride) {
+    const uint64_t d4[4] = {uint64_t(width), uint64_t(heads), uint64_t(len), uint64_t(batch)};
+    const uint64_t s4[3] = {uint64_t(head_stride) * 2, uint64_t(token_stride) * 2,
+                            uint64_t(token_stride) * uint64_t(len) * 2};
+    const uint32_t box[4] = {64, 1, 128, 1};
+    return encode_bf16_map(m, at, 4, d4, s4, box, CU_TENSOR_MAP_SWIZZLE_128B);
+  };
+  bool maps = map4(&p.tm_q, q, dn, H, q_len, dq, H * dq) &&
+              map4(&p.tm_k, k_nope, dn, H, kv_len, k_head_stride, k_token_stride) &&
+              map4(&p.tm_v, v, dv, H, kv_len, v_head_stride, v_token_stride);
+  if (maps && dr > 0)
+    maps = map4(&p.tm_qr, static_cast<const uint16_t*>(q) + dn, dr, H, q_len, dq, H * dq) &&
+           map4(&p.tm_kr, k_pe, dr, G, kv_len, dr, k_pe_token_stride);
+  if (!maps) return MLA_ERR_CUDA;
+  p.seq_lens = seq_lens;
+  p.q_lens = q_lens;
+  p.o = static_cast<uint16_t*>(o);
+  p.lse = lse;
+  p.dev_error = dev_error;
+  p.batch = batch;
+  p.q_len = q_len;
+  p.kv_len = kv_len;
+  p.heads = H;
+  p.heads_per_group = H / G;
+  p.dn = dn;
+  p.dr = dr;
+  p.dv = dv;
+  p.causal = causal;
+  p.scale_log2 = dims->softmax_scale * 1.4426950408889634f;
+  return launch_prefill(p, as_stream(stream)) == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+}
+
 mla_status mla_selftest_wait_timeout(int32_t* dev_error, void* stream) {
   if (!dev_error) return MLA_ERR_INVALID_ARG;
   mla_selftest_wait_kernel<<<1, 32, 0, as_stream(stream)>>>(dev_error);

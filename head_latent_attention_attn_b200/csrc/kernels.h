@@ -208,6 +208,22 @@ int decode_pair_max_clusters(size_t smem);
 cudaError_t launch_decode_pair(const DecodeParams& p, dim3 grid, size_t smem,
                                cudaStream_t stream);
 
+// ---- mla_prefill_attn: the expanded form (prefill.cu) --------------------------------------
+struct PrefillParams {
+  CUtensorMap tm_q, tm_qr;   // 4D {d_n or d_r, H, q_len, B} over q's two parts, box {64, 1, 128, 1}
+  CUtensorMap tm_k;          // 4D {d_n, H, kv_len, B}
+  CUtensorMap tm_kr;         // 4D {d_r, G, kv_len, B}
+  CUtensorMap tm_v;          // 4D {d_v, H, kv_len, B}
+  const int32_t* seq_lens;   // [B]
+  const int32_t* q_lens;     // [B] or null: all q_len
+  uint16_t* o;               // [B, q_len, H, d_v]
+  float* lse;                // [B, q_len, H]
+  int32_t* dev_error;
+  int32_t batch, q_len, kv_len, heads, heads_per_group, dn, dr, dv, causal;
+  float scale_log2;          // softmax_scale * log2(e)
+};
+cudaError_t launch_prefill(const PrefillParams& p, cudaStream_t stream);
+
 // Merge of the per-piece partials of units cut between CTAs (log-sum-exp identity).
 struct CombineParams {
   const uint16_t* part_o;    // bf16

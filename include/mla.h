@@ -284,6 +284,41 @@ mla_status mla_decode_attn_q8(const mla_dims* dims, const void* q_ext, const voi
                               void* o_latent, float* lse, void* stream);
 
 /*
+ * mla_prefill_attn - the same attention in its expanded form (eqs. (1)-(3) of the DeepSeek-V2
+ * page): a key and a value per head, the rotary key shared by the heads of a group. For a chunk
+ * of many new tokens this is the cheaper form: d_n + d_r + d_v multiplications a (query, token)
+ * pair and head instead of the absorbed form's 2 r + d_r. The keys and values of a context are
+ * expanded from its latents once a chunk (mla_out_up with W_UK, and with W_UV, on the rows that
+ * mla_cache_read_q8 returns or on the new tokens' c_kv).
+ *
+ *   q         bf16 [B, q, H, d_n + d_r]   query, its rotary part rotated
+ *   k_nope    bf16, token t of sequence b and head h at ((b*kv_len + t)*k_token_stride +
+ *             h*k_head_stride), d_n numbers (a packed [B, kv_len, H, d_n + d_v] serves as k_nope
+ *             and, d_n further, as v); strides in elements, multiples of 8
+ *   k_pe      bf16, ((b*kv_len + t)*k_pe_token_stride + g*d_r): rotated key of group g (the cache
+ *             rows of mla_cache_read_q8 from column r on: stride D). NULL when d_r = 0
+ *   v         bf16, as k_nope with its own strides, d_v numbers
+ *   seq_lens  int32 [B]  context length L of each sequence, in [0, kv_len]
+ *   q_lens    int32 [B] or NULL: query rows of each sequence, in [0, q] (a padded batch); NULL:
+ *             all q. Query row i of sequence b is at position L - q_lens[b] + i
+ *   o         bf16 [B, q, H, d_v] output; lse fp32 [B, q, H] output (natural logarithm). Rows
+ *             at and past q_lens[b] are left as they were
+ *   dev_error int32 device error word or NULL
+ * Row i sees token t < L, and with causal != 0 only t <= L - q_lens[b] + i; a row that sees none
+ * (L < q_lens[b], or L = 0) gives o = 0 and lse = -inf. What lies past L in k_nope, k_pe and v is
+ * not used. A NaN or infinity in the value of a token t < L makes o NaN also for the rows of its
+ * 128-row block that do not see t. A length out of range sets MLA_DEVERR_BOUNDS; that sequence
+ * then sees nothing. P is rounded to bf16 as a tensor-core operand; scores, sums and o are fp32.
+ * Requires d_n <= 128, d_v <= 128, d_r <= 64 and a multiple of 8 (MLA_ERR_UNSUPPORTED otherwise).
+ */
+mla_status mla_prefill_attn(const mla_dims* dims, const void* q, const void* k_nope,
+                            int64_t k_token_stride, int64_t k_head_stride, const void* k_pe,
+                            int64_t k_pe_token_stride, const void* v, int64_t v_token_stride,
+                            int64_t v_head_stride, const int32_t* seq_lens, const int32_t* q_lens,
+                            int32_t batch, int32_t q_len, int32_t kv_len, int32_t causal, void* o,
+                            float* lse, int32_t* dev_error, void* stream);
+
+/*
  * mla_decode_step - one whole decode step in one call: mla_cache_append, mla_absorb_q,
  * mla_decode_attn and mla_out_up on the same arguments, in that order (the absorbed
  * order of the DeepSeek-V2 page's "Matrix absorption" section, einsums (4) and (5)).

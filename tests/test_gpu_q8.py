@@ -239,11 +239,11 @@ def bounds_of(q, k, v, scale):
     """How far o and lse may be off (per row): scores are fp32 sums of exact products (each
     partial sum of the two-CTA kernel rounded by 2^-16 of it), so a score is off by
     d <= 2^-15 max_l scale |q| . |k_l|; exp2 and log2 are approximations to about 2^-21. A weight
-    is then off by d + 2^-9 (its bf16 rounding) relatively, and a piece and o by 2^-9 each."""
+    is then off by d + 2^-8 (its bf16 rounding) relatively, and a piece and o by 2^-8 each."""
     s = scale * (np.abs(q) @ np.abs(k).T).max(-1)
     d = 2.0 ** -15 * s + 2.0 ** -20
     top = np.abs(v).max()
-    return (2 * d + 2.0 ** -9 + 2.0 ** -14)[:, None] * top, 2.0 ** -8 * (1 + 2.0 ** -6), d
+    return (2 * d + 2.0 ** -8 + 2.0 ** -14)[:, None] * top, 2.0 ** -7 * (1 + 2.0 ** -6), d
 
 
 def check_attention(o, lse, q_bits, f, causal=True):
