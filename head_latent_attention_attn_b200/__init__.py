@@ -147,21 +147,33 @@ def _stream(stream) -> ctypes.c_void_p:
     return ctypes.c_void_p(int(stream))
 
 
-def _one_device(tensors, stream):
-    """Context of a call on the device that holds all of `tensors` (and `stream`, if it is a
-    torch stream), so that the launch goes to that device and to its current stream."""
-    dev = None
-    for t in tensors:
-        if t is None:
-            continue
-        if dev is None:
-            dev = t.device
-        elif t.device != dev:
-            raise MlaError(f"tensors are on {dev} and on {t.device}", MLA_ERR_INVALID_ARG)
-    if isinstance(stream, torch.cuda.Stream) and stream.device != dev:
-        raise MlaError(f"the stream is on {stream.device}, the tensors are on {dev}",
-                       MLA_ERR_INVALID_ARG)
-    return torch.cuda.device(dev)
+def _call(fn, what: str, stream, dims: MlaDims, *args) -> None:
+    """fn(dims, *args, stream) on the device that holds all tensors among `args` (passed as
+    their addresses), on `stream` or that device's current stream; raises on a status."""
+    dev, a = -1, []
+    for x in args:
+        if isinstance(x, torch.Tensor):
+            d = x.get_device()
+            if d != dev:
+                if dev >= 0:
+                    raise MlaError(f"{what}: tensors are on cuda:{dev} and cuda:{d}",
+                                   MLA_ERR_INVALID_ARG)
+                dev = d
+            x = x.data_ptr()
+        a.append(x)
+    if isinstance(stream, torch.cuda.Stream):
+        if stream.device.index != dev:
+            raise MlaError(f"{what}: the stream is on {stream.device}, the tensors on cuda:{dev}",
+                           MLA_ERR_INVALID_ARG)
+        stream = stream.cuda_stream
+    elif stream is None:
+        stream = torch.cuda.current_stream(dev).cuda_stream
+    if dev == torch.cuda.current_device():
+        st = fn(ctypes.byref(dims), *a, stream)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(ctypes.byref(dims), *a, stream)
+    _check(st, what)
 
 
 def _check(status: int, what: str) -> None:
@@ -172,13 +184,13 @@ def _check(status: int, what: str) -> None:
 def _need(t, name: str, dtype, shape=None, cuda: bool = True) -> None:
     if not isinstance(t, torch.Tensor):
         raise MlaError(f"{name} must be a torch.Tensor", MLA_ERR_INVALID_ARG)
-    if cuda and t.device.type != "cuda":
+    if cuda and not t.is_cuda:
         raise MlaError(f"{name} must be on a CUDA device", MLA_ERR_INVALID_ARG)
     if t.dtype != dtype:
         raise MlaError(f"{name} must be {dtype}, got {t.dtype}", MLA_ERR_INVALID_ARG)
     if not t.is_contiguous():
         raise MlaError(f"{name} must be contiguous", MLA_ERR_INVALID_ARG)
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:     # torch.Size is a tuple
         raise MlaError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}",
                        MLA_ERR_INVALID_ARG)
 
@@ -356,9 +368,7 @@ def mla_q8_page_bytes(dims: MlaDims) -> int:
 
 def _need_q8(dims: MlaDims, cache, block_table, B: int) -> None:
     _need(cache, "cache", torch.uint8)
-    want = mla_q8_page_bytes(dims)
-    if want < 0:
-        raise MlaError("dims cannot have an 8-bit cache", MLA_ERR_UNSUPPORTED)
+    want = dims.page_size * (2 * dims.row_width - dims.kv_lora_rank + 8)   # the call checks dims
     if cache.dim() != 2 or cache.shape[1] != want:
         raise MlaError(f"cache must be [num_pages, {want}], got {tuple(cache.shape)}",
                        MLA_ERR_INVALID_ARG)
@@ -389,13 +399,9 @@ def mla_cache_append_q8(dims: MlaDims, c_kv, k_r, rope_cos, rope_sin, block_tabl
         _need(new_lens, "new_lens", torch.int32, (B,))
     if dev_error is not None:
         _need(dev_error, "dev_error", torch.int32)
-    with _one_device((c_kv, k_r, rope_cos, rope_sin, block_table, start_pos, cache, new_lens,
-                      dev_error), stream):
-        st = lib().mla_cache_append_q8(ctypes.byref(dims), _ptr(c_kv), _ptr(k_r), _ptr(rope_cos),
-                                       _ptr(rope_sin), _ptr(block_table), block_table.shape[1],
-                                       _ptr(start_pos), _ptr(new_lens), B, n, _ptr(cache),
-                                       cache.shape[0], _ptr(dev_error), _stream(stream))
-    _check(st, "mla_cache_append_q8")
+    _call(lib().mla_cache_append_q8, "mla_cache_append_q8", stream, dims, c_kv, k_r, rope_cos,
+          rope_sin, block_table, block_table.shape[1], start_pos, new_lens, B, n, cache,
+          cache.shape[0], dev_error)
 
 
 def mla_cache_read_q8(dims: MlaDims, cache, block_table, start_pos, out, read_lens=None,
@@ -412,12 +418,8 @@ def mla_cache_read_q8(dims: MlaDims, cache, block_table, start_pos, out, read_le
         _need(read_lens, "read_lens", torch.int32, (B,))
     if dev_error is not None:
         _need(dev_error, "dev_error", torch.int32)
-    with _one_device((cache, block_table, start_pos, out, read_lens, dev_error), stream):
-        st = lib().mla_cache_read_q8(ctypes.byref(dims), _ptr(cache), cache.shape[0],
-                                     _ptr(block_table), block_table.shape[1], _ptr(start_pos),
-                                     _ptr(read_lens), B, n, _ptr(out), _ptr(dev_error),
-                                     _stream(stream))
-    _check(st, "mla_cache_read_q8")
+    _call(lib().mla_cache_read_q8, "mla_cache_read_q8", stream, dims, cache, cache.shape[0],
+          block_table, block_table.shape[1], start_pos, read_lens, B, n, out, dev_error)
 
 
 def mla_decode_attn_q8(dims: MlaDims, q_ext, cache, block_table, seq_lens, max_seq_len: int,
@@ -435,13 +437,9 @@ def mla_decode_attn_q8(dims: MlaDims, q_ext, cache, block_table, seq_lens, max_s
     _need(o_latent, "o_latent", torch.bfloat16, (B, q, H, r))
     _need(lse, "lse", torch.float32, (B, q, H))
     _need(workspace, "workspace", torch.uint8)
-    with _one_device((q_ext, cache, block_table, seq_lens, o_latent, lse, workspace), stream):
-        st = lib().mla_decode_attn_q8(ctypes.byref(dims), _ptr(q_ext), _ptr(cache), cache.shape[0],
-                                      _ptr(block_table), block_table.shape[1], _ptr(seq_lens), B,
-                                      q, int(max_seq_len), 1 if causal else 0, int(num_splits),
-                                      _ptr(workspace), workspace.numel(), _ptr(o_latent),
-                                      _ptr(lse), _stream(stream))
-    _check(st, "mla_decode_attn_q8")
+    _call(lib().mla_decode_attn_q8, "mla_decode_attn_q8", stream, dims, q_ext, cache,
+          cache.shape[0], block_table, block_table.shape[1], seq_lens, B, q, int(max_seq_len),
+          1 if causal else 0, int(num_splits), workspace, workspace.numel(), o_latent, lse)
 
 
 def _per_token(t, name: str, shape):
@@ -495,12 +493,9 @@ def mla_prefill_attn(dims: MlaDims, q, k_nope, k_pe, v, seq_lens, o, lse, q_lens
         _need(q_lens, "q_lens", torch.int32, (B,))
     if dev_error is not None:
         _need(dev_error, "dev_error", torch.int32)
-    with _one_device((q, k_nope, k_pe, v, seq_lens, o, lse, q_lens, dev_error), stream):
-        st = lib().mla_prefill_attn(
-            ctypes.byref(dims), _ptr(q), _ptr(k_nope), k_tok, k_head, _ptr(k_pe), kr_tok, _ptr(v),
-            v_tok, v_head, _ptr(seq_lens), _ptr(q_lens), B, ql, n, 1 if causal else 0, _ptr(o),
-            _ptr(lse), _ptr(dev_error), _stream(stream))
-    _check(st, "mla_prefill_attn")
+    _call(lib().mla_prefill_attn, "mla_prefill_attn", stream, dims, q, k_nope, k_tok, k_head, k_pe,
+          kr_tok, v, v_tok, v_head, seq_lens, q_lens, B, ql, n, 1 if causal else 0, o, lse,
+          dev_error)
 
 
 def mla_kv_shared_decode_dims(dims: MlaDims) -> MlaDims:

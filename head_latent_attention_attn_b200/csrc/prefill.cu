@@ -52,7 +52,7 @@ constexpr uint32_t kQGroup = 3 * kBlk;
 constexpr uint32_t kSlotOff = 2 * kQGroup;       // K unrotated / V, 2 blocks each
 constexpr uint32_t kRopeOff = kSlotOff + kSlots * 2 * kBlk;
 constexpr uint32_t kMiscOff = kRopeOff + 2 * kBlk;
-constexpr uint32_t kBars = 2 + 2 * kSlots + 6;
+constexpr uint32_t kBars = 2 + 2 * kSlots + 8;
 constexpr uint32_t kSmem = kMiscOff + 64 + 8 * kBars + 1024;   // + alignment slack
 static_assert(kSmem <= 232448, "shared memory of a CTA");
 
@@ -69,8 +69,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* full = q_full + 2;                   // [slot] K or V tile landed
   uint64_t* empty = full + kSlots;               // [slot]
   uint64_t* s_full = empty + kSlots;             // [group] scores computed
-  uint64_t* p_full = s_full + 2;                 // [group] weights written (4 warps)
-  uint64_t* pv_done = p_full + 2;                // [group] PV of the group's tile done
+  uint64_t* p_full = s_full + 2;                 // [group][half] weights of 64 tokens written
+  uint64_t* pv_done = p_full + 4;                // [group] PV of the group's tile done
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const WaitCtx wc{abort_flag, p.dev_error};
 
@@ -78,7 +78,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(&q_full[i], 1);
       mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], 4);
+      mbar_init(&p_full[2 * i], 4);              // the group's four warps
+      mbar_init(&p_full[2 * i + 1], 4);
       mbar_init(&pv_done[i], 1);
     }
     for (int i = 0; i < kSlots; ++i) {
@@ -198,14 +199,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           umma_commit(&s_full[g]);
         };
         auto values = [&](int g, int j) {
-          ok = ok && mbar_wait(&p_full[g], j & 1, wc);
-          if (!ok) return;
-          tc_fence_after();
           const uint64_t vd = v0 + ((((2 * j + 1) % kSlots) * 2 * kBlk) >> 4);
 #pragma unroll
-          for (int i = 0; i < kTok / 16; ++i)
+          for (int i = 0; i < kTok / 16; ++i) {
+            if (i % 4 == 0) {                     // the first half while the second is computed
+              ok = ok && mbar_wait(&p_full[2 * g + i / 4], j & 1, wc);
+              if (!ok) return;
+              tc_fence_after();
+            }
             umma_bf16_ts(tmem + kColO + 128 * g, tmem + kColS + 128 * g + 8 * i,
                          vd + ((i * 2048) >> 4), idesc_o, (j > 0 || i > 0) ? 1u : 0u);
+          }
           umma_commit(&pv_done[g]);
         };
         wait_unit(0);
@@ -266,12 +270,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       float mx[4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) mx[k] = fmaxf(s[k], s[k + 4]);
+      for (int i = 0; i < 4; ++i) mx[i] = max3(s[i], s[i + 4], s[i + 8]);
 #pragma unroll
-      for (int k = 8; k < kTok; k += 8)
+      for (int k = 12; k + 8 <= kTok; k += 8)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) mx[i] = fmaxf(mx[i], fmaxf(s[k + i], s[k + 4 + i]));
-      const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
+        for (int i = 0; i < 4; ++i) mx[i] = max3(mx[i], s[k + i], s[k + 4 + i]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) mx[i] = fmaxf(mx[i], s[kTok - 4 + i]);
+      const float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * c;
       float alpha = 1.0f;
       if (top > m + kLazyThreshold) {
         alpha = ex2_approx(m - top);             // 0 while m is still kRefInit
@@ -293,21 +299,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_st16(t_o + k, o);
         }
       }
-      float sum0 = 0.0f, sum1 = 0.0f;
-#pragma unroll
-      for (int k = 0; k < kTok; k += 32) {
-        uint32_t w[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const float a = ex2_approx(fmaf(s[k + 2 * i], c, -m));
-          const float d = ex2_approx(fmaf(s[k + 2 * i + 1], c, -m));
-          sum0 += a;
-          sum1 += d;
-          w[i] = cvt_bf16x2(a, d);
-        }
-        tmem_st16(t_s + k / 2, reinterpret_cast<const float*>(w));
-      }
-      l += sum0 + sum1;
       if (t0 + kTok > L) {
         // value rows past the context may hold anything (0-weight x NaN is NaN): zero them. Both
         // groups do so; the second writes zeros over zeros.
@@ -325,10 +316,30 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         fence_proxy_async_smem();
       }
-      tmem_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&p_full[g]);
+      // weights 2^(s * scale - m), in pairs, half a tile at a time
+      const float2 c2 = make_float2(c, c), m2 = make_float2(-m, -m);
+      float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+#pragma unroll
+        for (int k = 64 * half; k < 64 * half + 64; k += 32) {
+          uint32_t w[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            float2 e = fma_f32x2(make_float2(s[k + 2 * i], s[k + 2 * i + 1]), c2, m2);
+            e.x = ex2_approx(e.x);
+            e.y = ex2_approx(e.y);
+            sum[i & 1] = add_f32x2(sum[i & 1], e);
+            w[i] = cvt_bf16x2(e.x, e.y);
+          }
+          tmem_st16(t_s + k / 2, reinterpret_cast<const float*>(w));
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[2 * g + half]);
+      }
+      l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
     }
     // ------------------------------------ epilogue ---------------------------------------
     bool fin = true;
