@@ -975,7 +975,7 @@ mla_status mla_prefill_attn(const mla_dims* dims, const void* q, const void* k_n
       !strides_ok(v_token_stride, v_head_stride, dv, H) ||
       (dr > 0 && !strides_ok(k_pe_token_stride, dr, dr, G)))
     return MLA_ERR_INVALID_ARG;
-  if (H > 65535 || batch > 65535) return MLA_ERR_UNSUPPORTED;
+  if (int64_t(H) * batch * ((int64_t(q_len) + 255) / 256) > INT32_MAX) return MLA_ERR_UNSUPPORTED;
   PrefillParams p{};
   const int64_t dq = dn + dr;
   auto map4 = [&](CUtensorMap* m, const void* at, int width, int heads, int64_t len,
@@ -1007,6 +1007,9 @@ mla_status mla_prefill_attn(const mla_dims* dims, const void* q, const void* k_n
   p.dr = dr;
   p.dv = dv;
   p.causal = causal;
+  // half of the 126 MB L2 for the keys and values of the heads in work
+  p.head_block = int32_t(std::max<int64_t>(
+      1, std::min<int64_t>(int64_t(H) * batch, (int64_t(64) << 20) / (int64_t(kv_len) * (dn + dv) * 2))));
   p.scale_log2 = dims->softmax_scale * 1.4426950408889634f;
   return launch_prefill(p, as_stream(stream)) == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }

@@ -220,6 +220,7 @@ struct PrefillParams {
   float* lse;                // [B, q_len, H]
   int32_t* dev_error;
   int32_t batch, q_len, kv_len, heads, heads_per_group, dn, dr, dv, causal;
+  int32_t head_block;        // heads whose keys and values are worked on together
   float scale_log2;          // softmax_scale * log2(e)
 };
 cudaError_t launch_prefill(const PrefillParams& p, cudaStream_t stream);

@@ -207,6 +207,33 @@ MLA_DEVICE void tma_prefetch_l2_3d(const CUtensorMap* map, int32_t x, int32_t y,
 }
 
 // ---------------------------------------------------------------------------------------
+// Cluster launch control: a running CTA takes over the work of a CTA of its grid that has not
+// been launched yet. try_cancel asks for one; its 16-byte answer lands at `resp` (shared memory,
+// 16-byte aligned) and completes 16 bytes on `bar`. cancelled_cta reads the answer: the
+// blockIdx.x taken over, or -1 when none was left (then no further request may be made).
+// ---------------------------------------------------------------------------------------
+MLA_DEVICE void try_cancel_cta(void* resp, uint64_t* bar) {
+  asm volatile(
+      "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128"
+      " [%0], [%1];" ::"r"(smem_u32(resp)),
+      "r"(smem_u32(bar))
+      : "memory");
+}
+MLA_DEVICE int cancelled_cta(const void* resp) {
+  uint32_t ok, x;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b128 r;\n\t"
+      "ld.shared.b128 r, [%2];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\tmov.u32 %1, 0;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, r;\n\t}"
+      : "=r"(ok), "=r"(x)
+      : "r"(smem_u32(resp))
+      : "memory");
+  return ok ? int(x) : -1;
+}
+
+// ---------------------------------------------------------------------------------------
 // Programmatic dependent launch. Every kernel here is launched so that it may start while
 // the kernel before it on the stream is still running. Each thread calls grid_dep_wait()
 // before its first access to global memory that another kernel may write (inputs, outputs,
@@ -319,6 +346,12 @@ MLA_DEVICE bool mbar_wait_cluster(uint64_t* bar, uint32_t parity, const WaitCtx&
       return false;
     }
   }
+}
+// A float of another CTA's shared memory (address from map_to_rank).
+MLA_DEVICE float ld_cluster_f32(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
 }
 MLA_DEVICE uint4 ld_shared_v4(uint32_t saddr) {
   uint4 v;
