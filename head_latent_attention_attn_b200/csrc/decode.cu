@@ -70,6 +70,9 @@ template <bool Q8>
 constexpr int kSmWarp0 = Q8 ? 4 : 2;                 // first of the four softmax warps
 constexpr int kDqWarp0 = 8, kDqWarps = 16;
 constexpr int kRegsLaunch = 80, kRegsIssue = 40, kRegsSoftmax = 216, kRegsDequant = 56;
+// setmaxnreg may only lower a group's share by .dec and raise it by .inc
+static_assert(kRegsIssue <= kRegsLaunch && kRegsDequant <= kRegsLaunch &&
+              kRegsSoftmax >= kRegsLaunch, "register shares");
 static_assert(kRegsIssue + kRegsSoftmax + (kDqWarps / 4) * kRegsDequant <=
                   (2 + kDqWarps / 4) * kRegsLaunch,
               "the groups' registers exceed what the block is launched with");
@@ -418,8 +421,8 @@ __global__ void __launch_bounds__(kBlockThreads<Q8>, 1)
     if (has_work) {
       const int wi = warp - kDqWarp0, lb = p.r / kQ8Cols;
       const int half = (lb + 1) / 2, blk0 = wi < 8 ? 0 : half;
-      dequant_pages(p, cg, r0, r1, sched[0], sched[1], wi & 7, blk0, wi < 8 ? half : lb - half,
-                    blk0, slots, slot_bytes, full, empty, wc);
+      dequant_pages<1>(p, cg, r0, r1, sched[0], sched[1], wi & 7, blk0, wi < 8 ? half : lb - half,
+                       blk0, slots, slot_bytes, full, empty, wc);
     }
   } else {
   if constexpr (Q8) reg_inc<kRegsSoftmax>();
@@ -684,6 +687,10 @@ extern "C" int mla_trace_read(unsigned long long* host, int n) {
 template <int NCOL, bool Q8>
 static cudaError_t launch_decode_n(const DecodeParams& p, dim3 grid, size_t smem,
                                    cudaStream_t stream) {
+  if (Q8) {
+    static const bool regs_ok = launched_with_regs(mla_decode_kernel<NCOL, Q8>, kRegsLaunch);
+    if (!regs_ok) return cudaErrorInvalidDeviceFunction;
+  }
   cudaError_t e = cudaFuncSetAttribute(mla_decode_kernel<NCOL, Q8>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
   if (e != cudaSuccess) return e;

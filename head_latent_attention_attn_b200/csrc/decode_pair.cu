@@ -38,6 +38,8 @@
 //              for those rows into TMEM, and their epilogue.
 #include <math.h>
 
+#include <type_traits>
+
 #include "decode_sched.cuh"
 #include "dequant.cuh"
 #include "kernels.h"
@@ -78,8 +80,12 @@ constexpr int kRowWarp0 = Q8 ? 4 : 3;
 constexpr int kDqWarp0 = kRowWarp0<true> + 12, kDqWarps = 8;
 template <bool Q8>
 constexpr int kThreads = 32 * (Q8 ? kDqWarp0 + kDqWarps : kRowWarp0<Q8> + 12);
-constexpr int kRegsLaunch = 80, kRegsIssue = 40, kRegsOwner = 128, kRegsSender = 96,
-              kRegsReceiver = 96, kRegsDequant = 56;
+constexpr int kRegsLaunch = 80, kRegsIssue = 56, kRegsOwner = 128, kRegsSender = 88,
+              kRegsReceiver = 88, kRegsDequant = 56;
+// setmaxnreg may only lower a group's share by .dec and raise it by .inc
+static_assert(kRegsIssue <= kRegsLaunch && kRegsDequant <= kRegsLaunch &&
+              kRegsOwner >= kRegsLaunch && kRegsSender >= kRegsLaunch &&
+              kRegsReceiver >= kRegsLaunch, "register shares");
 static_assert(kRegsIssue + kRegsOwner + kRegsSender + kRegsReceiver +
                       (kDqWarps / 4) * kRegsDequant <= (4 + kDqWarps / 4) * kRegsLaunch,
               "the groups' registers exceed what the block is launched with");
@@ -493,15 +499,17 @@ __global__ void __launch_bounds__(kThreads<Q8>, 1)
     // ============================== dequantising warps (Q8) ==============================
     if constexpr (Q8) reg_dec<kRegsDequant>();
     if (has_work)
-      dequant_pages(p, cg, r0, r1, sched[0], sched[1], warp - kDqWarp0, int(rank) * lb, lb, 0,
-                    slots, lay.slot_bytes, full, empty, wc);
+      dequant_pages<8 / kDqWarps>(p, cg, r0, r1, sched[0], sched[1],
+                                  (warp - kDqWarp0) * (8 / kDqWarps), int(rank) * lb, lb, 0, slots,
+                                  lay.slot_bytes, full, empty, wc);
   } else if (has_work) {
+    auto rows = [&](auto role_tag) {
+    constexpr int role = decltype(role_tag)::value;   // 0 owner, 1 sender, 2 receiver
     // ==================================== the 128 rows ====================================
     // Every row warp works on 16 TMEM lanes of its sub-partition with 16x32bx2 accesses:
     // lanes i and i + 16 of the warp share row i and take tokens 0-31 and 32-63 (or the
     // two 16-column halves of every 32 columns of O).
     const int sp = warp & 3;                  // TMEM sub-partition this warp reaches
-    const int role = (warp - kRowWarp0<Q8>) >> 2; // 0 owner, 1 sender, 2 receiver
     const int qt = lane >> 4;                 // token half of this thread
     const int i16 = lane & 15;
     // owners work on this CTA's rows, senders and receivers on the partner's
@@ -626,8 +634,7 @@ __global__ void __launch_bounds__(kThreads<Q8>, 1)
       tc_fence_before();
     };
 
-    if (role == 0) {
-      if constexpr (Q8) reg_inc<kRegsOwner>();
+    if constexpr (role == 0) {
       // ------------- owner: this CTA's 16 rows of sub-partition sp; softmax and P ---------
       const int qi = row / p.num_heads;
       load_q(sched[0]);
@@ -780,8 +787,7 @@ __global__ void __launch_bounds__(kThreads<Q8>, 1)
         if (w.s >= r1) break;
         w.load(p, cg);
       }
-    } else if (role == 1) {
-      if constexpr (Q8) reg_inc<kRegsSender>();
+    } else if constexpr (role == 1) {
       // ------------- sender: the partner's 16 rows of sub-partition sp, partial scores ----
       load_q(sched[0]);
       UnitWalk w{sched[0], sched[1]};
@@ -826,7 +832,6 @@ __global__ void __launch_bounds__(kThreads<Q8>, 1)
         }
       }
     } else {
-      if constexpr (Q8) reg_inc<kRegsReceiver>();
       // ------------- receiver: the partner's weights for its 16 rows of sub-partition sp --
       UnitWalk w{sched[0], sched[1]};
       w.load(p, cg);
@@ -880,6 +885,18 @@ __global__ void __launch_bounds__(kThreads<Q8>, 1)
         w.load(p, cg);
       }
     }
+    };
+    const int role = (warp - kRowWarp0<Q8>) >> 2;
+    if (role == 0) {
+      if constexpr (Q8) reg_inc<kRegsOwner>();
+      rows(std::integral_constant<int, 0>{});
+    } else if (role == 1) {
+      if constexpr (Q8) reg_inc<kRegsSender>();
+      rows(std::integral_constant<int, 1>{});
+    } else {
+      if constexpr (Q8) reg_inc<kRegsReceiver>();
+      rows(std::integral_constant<int, 2>{});
+    }
   }
 
   tc_fence_before();
@@ -931,6 +948,10 @@ int decode_pair_max_clusters(size_t smem) {
 template <bool Q8>
 static cudaError_t launch_decode_pair_t(const DecodeParams& p, dim3 grid, size_t smem,
                                         cudaStream_t stream) {
+  if (Q8) {
+    static const bool regs_ok = launched_with_regs(mla_decode_pair_kernel<Q8>, kRegsLaunch);
+    if (!regs_ok) return cudaErrorInvalidDeviceFunction;
+  }
   cudaError_t e = cudaFuncSetAttribute(mla_decode_pair_kernel<Q8>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
   if (e != cudaSuccess) return e;

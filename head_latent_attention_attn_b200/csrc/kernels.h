@@ -39,6 +39,15 @@ inline cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, s
   return cudaGetLastError();
 }
 
+// Whether `kernel` is launched with exactly `regs` registers a thread: kernels that move registers
+// between their warps (setmaxnreg) add up shares of that number, and would wait forever for
+// registers that the block was not given. A property of the build; callers ask once.
+template <typename K>
+inline bool launched_with_regs(K* kernel, int regs) {
+  cudaFuncAttributes a = {};
+  return cudaFuncGetAttributes(&a, kernel) == cudaSuccess && a.numRegs == regs;
+}
+
 // ---- mla_cache_append -------------------------------------------------------------------
 struct AppendParams {
   const uint16_t* c_kv;      // [B, n_new, r]

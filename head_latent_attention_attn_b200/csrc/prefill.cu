@@ -47,6 +47,8 @@ constexpr uint32_t kBlk = 128 * 128;             // 128 rows x 64 bf16, 16 KB
 constexpr int kSlots = 3;
 constexpr uint32_t kColO = 0, kColS = 256;       // + 128 g
 constexpr int kRegsLaunch = 168, kRegsIssue = 72, kRegsRows = 216;
+// setmaxnreg may only lower a group's share by .dec and raise it by .inc
+static_assert(kRegsIssue <= kRegsLaunch && kRegsRows >= kRegsLaunch, "register shares");
 static_assert(kRegsIssue + 2 * kRegsRows <= 3 * kRegsLaunch,
               "the groups' registers exceed what the block is launched with");
 constexpr float kLazyThreshold = 8.0f;           // log2 units
@@ -538,6 +540,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 cudaError_t launch_prefill(const PrefillParams& p, cudaStream_t stream) {
+  static const bool regs_ok = launched_with_regs(mla_prefill_kernel, kRegsLaunch);
+  if (!regs_ok) return cudaErrorInvalidDeviceFunction;
   const cudaError_t e = cudaFuncSetAttribute(
       mla_prefill_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kSmem));
   if (e != cudaSuccess) return e;
