@@ -38,7 +38,7 @@ C_SYMBOLS = ("mla_row_width", "mla_status_string", "mla_cache_append", "mla_abso
              "mla_kv_shared_decode_dims", "mla_kv_shared_query", "mla_kv_shared_output",
              "mla_down_kv_append", "mla_out_proj_workspace_size",
              "mla_out_proj", "mla_decode_step", "mla_q8_page_bytes", "mla_cache_append_q8",
-             "mla_cache_read_q8", "mla_decode_attn_q8", "mla_prefill_attn")
+             "mla_cache_read_q8", "mla_decode_attn_q8", "mla_prefill_attn", "mla_decode_q8_workspace_size")
 
 
 class MlaError(RuntimeError):
@@ -128,6 +128,8 @@ def lib() -> ctypes.CDLL:
     L.mla_cache_read_q8.restype = _I32
     L.mla_decode_attn_q8.argtypes = L.mla_decode_attn.argtypes
     L.mla_decode_attn_q8.restype = _I32
+    L.mla_decode_q8_workspace_size.argtypes = L.mla_decode_workspace_size.argtypes
+    L.mla_decode_q8_workspace_size.restype = ctypes.c_size_t
     L.mla_prefill_attn.argtypes = [D, _P, _P, _I64, _I64, _P, _I64, _P, _I64, _I64, _P, _P, _I32,
                                    _I32, _I32, _I32, _P, _P, _P, _P]
     L.mla_prefill_attn.restype = _I32
@@ -422,11 +424,19 @@ def mla_cache_read_q8(dims: MlaDims, cache, block_table, start_pos, out, read_le
           block_table, block_table.shape[1], start_pos, read_lens, B, n, out, dev_error)
 
 
+def mla_decode_q8_workspace_size(dims: MlaDims, batch: int, q_len: int, max_seq_len: int,
+                                 num_splits: int = 0) -> int:
+    """Workspace with which mla_decode_attn_q8 converts every page once for many query rows."""
+    return int(lib().mla_decode_q8_workspace_size(ctypes.byref(dims), batch, q_len, max_seq_len,
+                                                  num_splits))
+
+
 def mla_decode_attn_q8(dims: MlaDims, q_ext, cache, block_table, seq_lens, max_seq_len: int,
                        workspace, o_latent, lse, causal: bool = True, num_splits: int = 0,
                        stream=None) -> None:
     """mla_decode_attn over the 8-bit cache [P, mla_q8_page_bytes]: o_latent [B, q, H, r] (bf16)
-    and lse [B, q, H] (fp32); the workspace is mla_decode_workspace_size's."""
+    and lse [B, q, H] (fp32); the workspace is mla_decode_workspace_size's, or for a chunk of many
+    rows better mla_decode_q8_workspace_size's."""
     if not isinstance(q_ext, torch.Tensor) or q_ext.dim() != 4:
         raise MlaError("q_ext must be a tensor [B, q, H, D]", MLA_ERR_INVALID_ARG)
     B, q = q_ext.shape[0], q_ext.shape[1]
@@ -649,4 +659,4 @@ __all__ = ["MlaDims", "MlaError", "make_dims", "lib", "mla_row_width", "mla_cach
            "mla_out_proj_workspace_size",
            "mla_out_proj", "mla_get_device_status", "mla_decode_step", "mla_q8_page_bytes",
            "mla_cache_append_q8", "mla_cache_read_q8", "mla_decode_attn_q8", "mla_prefill_attn",
-           "C_SYMBOLS", "STATUS_NAMES"]
+           "mla_decode_q8_workspace_size", "C_SYMBOLS", "STATUS_NAMES"]

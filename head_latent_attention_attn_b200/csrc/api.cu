@@ -688,6 +688,29 @@ mla_status build_decode(const mla_dims* dims, const void* q_ext, const void* cac
   return MLA_OK;
 }
 
+// Where mla_decode_attn_q8 may put the contexts' rows in bf16 (behind them their block table), so
+// that each page is converted once and not by every block of query rows that reads it. On B200
+// the conversion in the decode kernel makes the two-CTA kernel 1.4 times slower (64 x 8192
+// tokens, 128 heads: 261 us, 188 us over bf16 rows), while a pass that writes the rows first
+// costs 0.75 of such a block's time; from three blocks on (off != 0) it pays: a chunk of 256
+// rows of 128 heads over 4096 tokens takes 530 us with 256 conversions of every page.
+struct RowsPlan {
+  size_t off, table_off, bytes;
+  int32_t tiles;
+};
+
+RowsPlan plan_rows(const mla_dims* d, const DecodePlan& P, int32_t batch, int32_t max_seq_len) {
+  RowsPlan C{};
+  C.tiles = (max_seq_len + kDecodeTok - 1) / kDecodeTok;
+  const int64_t tokens = int64_t(batch) * C.tiles * kDecodeTok;
+  if (P.col_groups < 3 || batch == 0 || tokens > (int64_t(1) << 31) - kDecodeTok) return C;
+  // a plan with one range per block of query rows cuts no sequence: its partials go unused
+  C.off = P.vgrid == P.col_groups ? P.part_o_off : align256(P.ws_bytes);
+  C.table_off = align256(size_t(tokens) * row_width(d) * 2);
+  C.bytes = C.table_off + size_t(batch) * C.tiles * sizeof(int32_t);
+  return C;
+}
+
 // The decode kernel of a built plan and, when units may be cut between CTAs, the merge (which
 // then also brings `pf_bytes` at `pf`, the next kernel's weights, into L2; may be null).
 mla_status launch_decode_plan(const DecodePlan& P, const DecodeParams& p, cudaStream_t s,
@@ -752,12 +775,44 @@ mla_status mla_decode_attn_q8(const mla_dims* dims, const void* q_ext, const voi
   DecodePlan P;
   DecodeParams p;
   bool empty = false;
-  const mla_status st = build_decode(dims, q_ext, cache, num_pages, block_table,
-                                     max_pages_per_seq, seq_lens, batch, q_len, max_seq_len,
-                                     causal, num_splits, workspace, workspace_bytes, o_latent,
-                                     lse, &P, &p, &empty, true, true);
+  mla_status st = build_decode(dims, q_ext, cache, num_pages, block_table, max_pages_per_seq,
+                               seq_lens, batch, q_len, max_seq_len, causal, num_splits, workspace,
+                               workspace_bytes, o_latent, lse, &P, &p, &empty, true, true);
   if (st != MLA_OK || empty) return st;
+  const RowsPlan C = plan_rows(dims, P, batch, max_seq_len);
+  if (C.off == 0 || workspace_bytes < C.off + C.bytes || max_pages_per_seq < C.tiles)
+    return launch_decode_plan(P, p, as_stream(stream));
+  // every page to bf16 once, then the bf16 kernels over those rows
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  ReadQ8Params rp{};
+  rp.cache = static_cast<const uint8_t*>(cache);
+  rp.block_table = block_table;
+  rp.read_lens = seq_lens;
+  rp.out = reinterpret_cast<uint16_t*>(ws + C.off);
+  rp.out_table = reinterpret_cast<int32_t*>(ws + C.off + C.table_off);
+  rp.dev_error = reinterpret_cast<int32_t*>(ws);
+  rp.num_pages = num_pages;
+  rp.max_pages = max_pages_per_seq;
+  rp.batch = batch;
+  rp.n = C.tiles * kDecodeTok;
+  rp.r = dims->kv_lora_rank;
+  rp.R = row_width(dims) - rp.r;
+  st = build_decode(dims, q_ext, rp.out, int64_t(batch) * C.tiles, rp.out_table, C.tiles, seq_lens,
+                    batch, q_len, max_seq_len, causal, num_splits, workspace, workspace_bytes,
+                    o_latent, lse, &P, &p, &empty);
+  if (st != MLA_OK) return st;
+  if (launch_cache_read_q8(rp, as_stream(stream)) != cudaSuccess) return MLA_ERR_CUDA;
   return launch_decode_plan(P, p, as_stream(stream));
+}
+
+size_t mla_decode_q8_workspace_size(const mla_dims* dims, int32_t batch, int32_t q_len,
+                                    int32_t max_seq_len, int32_t num_splits) {
+  DecodePlan P;
+  if (check_q8(dims) != MLA_OK ||
+      plan_decode(dims, batch, q_len, max_seq_len, num_splits, &P) != MLA_OK)
+    return 0;
+  const RowsPlan C = plan_rows(dims, P, batch, max_seq_len);
+  return std::max(P.ws_bytes, C.off == 0 ? 0 : C.off + C.bytes);
 }
 
 int64_t mla_q8_page_bytes(const mla_dims* dims) {

@@ -113,11 +113,13 @@ __global__ void __launch_bounds__(256) cache_read_q8_kernel(ReadQ8Params p) {
   const int b = int(gw / per_seq);
   if (b >= p.batch) return;
   const int t = int(gw - int64_t(b) * per_seq) * 8 + (lane >> 2), part = lane & 3;
+  if (p.out_table && lane == 0 && t % kQ8Tok == 0)
+    p.out_table[int64_t(b) * (p.n / kQ8Tok) + t / kQ8Tok] = b * (p.n / kQ8Tok) + t / kQ8Tok;
   if (t >= q8_rows(p.read_lens, b, p.n, lane == 0 && t == 0 ? p.dev_error : nullptr)) return;
   int64_t page;
   int slot;
   if (!q8_locate(p.block_table, p.max_pages, p.num_pages, part == 0 ? p.dev_error : nullptr, b,
-                 int64_t(p.start_pos[b]) + t, &page, &slot))
+                 (p.start_pos ? int64_t(p.start_pos[b]) : 0) + t, &page, &slot))
     return;
   const int R = p.R, nb = p.r / kQ8Cols;
   const uint8_t* src = p.cache + page * q8_page_bytes(p.r, R);

@@ -82,9 +82,11 @@ cudaError_t launch_cache_append_q8(const AppendQ8Params& p, cudaStream_t stream)
 struct ReadQ8Params {
   const uint8_t* cache;
   const int32_t* block_table;
-  const int32_t* start_pos;
+  const int32_t* start_pos;  // [B], or null: 0
   const int32_t* read_lens;  // [B] rows to read of each sequence, or null: all n
   uint16_t* out;             // [B, n, r + R]
+  // [B, n / 64] or null: receives the block table of `out` as a bf16 cache of 64-token pages
+  int32_t* out_table;
   int32_t* dev_error;
   int64_t num_pages;
   int32_t max_pages, batch, n, r, R;

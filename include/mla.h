@@ -263,8 +263,15 @@ mla_status mla_decode_attn(const mla_dims* dims, const void* q_ext, const void* 
  * mla_decode_attn_q8 - mla_decode_attn over the 8-bit cache: the same arguments, plan and
  * workspace (mla_decode_workspace_size), for one query token, a few drafted ones or a whole
  * chunk. It gives the bits that mla_decode_attn gives over a bf16 cache of the rows that
- * mla_cache_read_q8 returns.
+ * mla_cache_read_q8 returns. With more than two blocks of query rows a sequence (a block is 128
+ * rows of q*H, 64 where the two-CTA kernel does not apply) a larger workspace
+ * (mla_decode_q8_workspace_size) lets it convert every page once instead of once a block.
+ *
+ * mla_decode_q8_workspace_size - that larger size (equal to mla_decode_workspace_size's where it
+ * would not help; 0 on invalid input). It grows with batch * max_seq_len rows of D bf16 numbers.
  */
+size_t mla_decode_q8_workspace_size(const mla_dims* dims, int32_t batch, int32_t q_len,
+                                    int32_t max_seq_len, int32_t num_splits);
 int64_t mla_q8_page_bytes(const mla_dims* dims);
 mla_status mla_cache_append_q8(const mla_dims* dims, const void* c_kv, const void* k_r,
                                const float* rope_cos, const float* rope_sin,

@@ -99,11 +99,12 @@ class Filled:
         return to_bits(x)
 
 
-def decode(dims, fn, q_bits, cache, table, lens, causal=True, num_splits=0, stream=None):
+def decode(dims, fn, q_bits, cache, table, lens, causal=True, num_splits=0,
+           size=mla.mla_decode_workspace_size):
     B, q, H, _ = q_bits.shape
     o = torch.full((B, q, H, dims.kv_lora_rank), 7.0, dtype=torch.bfloat16, device="cuda")
     lse = torch.full((B, q, H), 7.0, device="cuda")
-    n = mla.mla_decode_workspace_size(dims, B, q, max(lens), num_splits)
+    n = size(dims, B, q, max(lens), num_splits)
     ws = torch.zeros(n, dtype=torch.uint8, device="cuda")
     fn(dims, bf(q_bits), cache, cu(table), cu(np.array(lens, np.int32)), max(lens), ws, o, lse,
        causal=causal, num_splits=num_splits)
@@ -298,6 +299,44 @@ def test_decode_equals_bf16_cache_and_formula(name, lens, q, causal):
         assert torch.equal(o, o2) and torch.equal(lse, lse2), f"splits {ns}"
         check_attention(o, lse, q_bits, f, causal)
     assert mla.mla_get_device_status(f.err) == mla.MLA_OK
+
+
+@pytest.mark.parametrize("name,lens,q,ns", [
+    ("deepseek_v2", [300, 90, 80], 80, 0),       # one range a block: the rows lie over the partials
+    ("deepseek_v2", [300, 5, 64], 4, 0),         # sequences cut between ranges: behind them
+    ("deepseek_v2", [300, 5, 64], 4, 3),
+    ("hybrid", [700, 33], 33, 0),
+    ("rank_192", [130, 64], 9, 0),               # 64-row blocks of the one-CTA kernel
+    ("deepseek_v2", [130, 64], 2, 0),            # two blocks: nothing to gain, the same size
+])
+def test_pages_converted_once(name, lens, q, ns):
+    """The larger workspace gives the same bits, again and with what the last call left in it."""
+    f = Filled(name, lens, seed=q)
+    q_bits = f.query(q)
+    plain = mla.mla_decode_workspace_size(f.dims, len(lens), q, max(lens), ns)
+    large = mla.mla_decode_q8_workspace_size(f.dims, len(lens), q, max(lens), ns)
+    assert large >= plain and (large > plain or q in (2, 80))
+    want = decode(f.dims, mla.mla_decode_attn, q_bits, f.bf16_cache(), f.table, f.lens, True, ns)
+    for _ in range(2):
+        got = decode(f.dims, mla.mla_decode_attn_q8, q_bits, f.cache, f.table, f.lens, True, ns,
+                     mla.mla_decode_q8_workspace_size)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    B, H, r = len(lens), f.dims.num_heads, f.dims.kv_lora_rank
+    ws = torch.full((large,), 0xFF, dtype=torch.uint8, device="cuda")
+    ws[:4] = 0
+    o = torch.empty((B, q, H, r), dtype=torch.bfloat16, device="cuda")
+    lse = torch.empty((B, q, H), device="cuda")
+    table = f.table.copy()
+    for bad in (False, True):                    # a page id out of range: flagged, the others right
+        if bad:
+            table[1, 0] = f.P + 5
+        mla.mla_decode_attn_q8(f.dims, bf(q_bits), f.cache, cu(table), cu(np.array(f.lens, np.int32)),
+                               max(lens), ws, o, lse, num_splits=ns)
+        st = mla.mla_get_device_status(ws.view(torch.int32)[:1], reset=True)
+        assert st == (mla.MLA_ERR_DEVICE_BOUNDS if bad else mla.MLA_OK)
+        for b in range(B):
+            if not (bad and b == 1):
+                assert torch.equal(o[b], want[0][b]) and torch.equal(lse[b], want[1][b])
 
 
 @pytest.mark.parametrize("name", ["deepseek_v2", "qwen3_30b_a3b"])
