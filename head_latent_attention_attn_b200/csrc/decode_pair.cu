@@ -180,6 +180,14 @@ MLA_DEVICE void store_qlat(uint8_t* qlat, int n, int e, const uint32_t* v) {
   }
 }
 
+// Address of a remote barrier that a relaxed arrival releases a receive buffer on, made to depend
+// on the words read from the buffer (`zero` is 0 at run time): the arrival is then issued only
+// once the loads have returned. Without that the loads may still be queued behind other warps'
+// shared-memory traffic when the partner, told that the buffer is free, overwrites it.
+MLA_DEVICE uint32_t released_by(uint32_t remote_bar, uint32_t words, uint32_t zero) {
+  return remote_bar + (words & zero);
+}
+
 MLA_DEVICE void st_async_v2(uint32_t remote_addr, uint2 v, uint32_t remote_bar) {
   asm volatile(
       "st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.b32 [%0], {%1, %2}, [%3];"
@@ -674,6 +682,7 @@ __global__ void __launch_bounds__(kThreads<Q8>, 1)
           const bool rcv =
               __all_sync(0xffffffffu, mbar_wait_cluster(&xs_full[sb], (jj >> 1) & 1, wc));
           if (tr) MLA_PTRACE(5, jj);
+          uint32_t read_words = 0;
           {
             const uint32_t src = xs_s + sb * kXsBytes;
             uint32_t wb[kPackWords];
@@ -681,6 +690,7 @@ __global__ void __launch_bounds__(kThreads<Q8>, 1)
             for (int c = 0; c < kPackWords / 4; ++c) {
               const uint4 v = ld_shared_v4(src + xs_offset(sp, lane, c));
               wb[4 * c] = v.x; wb[4 * c + 1] = v.y; wb[4 * c + 2] = v.z; wb[4 * c + 3] = v.w;
+              read_words |= v.x;                 // a word of every load
             }
 #pragma unroll
             for (int g = 0; g < kHalfTok / 4; ++g) {
@@ -694,7 +704,9 @@ __global__ void __launch_bounds__(kThreads<Q8>, 1)
           // The received words are in registers: release the buffer to the partner without a
           // release fence (which would wait for this warp's remote stores), and re-arm it for
           // tile jj + 2 (the partner sends that only after all four owner warps released it).
-          if (lane == 1) mbar_arrive_remote_relaxed(sb ? xs_free_r1 : xs_free_r0);
+          if (lane == 1)
+            mbar_arrive_remote_relaxed(
+                released_by(sb ? xs_free_r1 : xs_free_r0, read_words, p.zero));
           if (sp == 0 && lane == 0 && rcv) mbar_arrive_expect_tx_relaxed(&xs_full[sb], kXsBytes);
 
           // ---- online softmax of row n over this tile (log2 domain, lazy reference) ----
@@ -844,14 +856,17 @@ __global__ void __launch_bounds__(kThreads<Q8>, 1)
           const bool rcv = __all_sync(0xffffffffu, mbar_wait_cluster(xp_full, jj & 1, wc));
           if (tr) MLA_PTRACE(7, jj);
           uint32_t pk[kHalfTok / 2];
+          uint32_t read_words = 0;               // a word of every load
           float alpha = 1.0f;
           if (rcv) {
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               const uint4 v = ld_shared_v4(xp_s + xp_offset(m, 4 * qt + k));
               pk[4 * k] = v.x; pk[4 * k + 1] = v.y; pk[4 * k + 2] = v.z; pk[4 * k + 3] = v.w;
+              read_words |= v.x;
             }
             const uint2 sv = ld_shared_v2(xp_s + xp_scalars(m));
+            read_words |= sv.x;
             alpha = __uint_as_float(sv.x);
             lt = __uint_as_float(sv.y);
           } else {
@@ -861,7 +876,7 @@ __global__ void __launch_bounds__(kThreads<Q8>, 1)
           }
           __syncwarp();
           // consumed into registers: release the buffer (relaxed) and re-arm it for tile jj + 1
-          if (lane == 1) mbar_arrive_remote_relaxed(xp_free_r);
+          if (lane == 1) mbar_arrive_remote_relaxed(released_by(xp_free_r, read_words, p.zero));
           if (sp == 0 && lane == 0 && rcv) mbar_arrive_expect_tx_relaxed(xp_full, kXpBytes);
           // the owner moved its reference: rescale these rows of this CTA's O half the same way
           if (t > tb && __any_sync(0xffffffffu, alpha != 1.0f)) rescale_o(jj, alpha);

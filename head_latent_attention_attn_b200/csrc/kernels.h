@@ -192,6 +192,7 @@ struct DecodeParams {
   int32_t max_pages, batch, q_len, num_heads, qH, r, D, nblk, nch, col_groups, units,
       max_seq_len, causal, nslot, slot_blocks, tmem_cols, npt;
   float scale_log2;          // softmax_scale * log2(e)
+  uint32_t zero;             // 0, which the compiler does not know (see released_by)
   // The 8-bit cache (q8.cuh): its pages, or null for the bf16 cache. tm_cache is then unused
   // and tm_rope covers the pages' key planes, 3D {R, 64, num_pages}.
   const void* cache_q8;

@@ -421,3 +421,17 @@ def test_graph_replay_and_side_streams(name):
     torch.cuda.synchronize()
     for i in range(2):
         assert torch.equal(outs[i][0], want[i][0]) and torch.equal(outs[i][1], want[i][1])
+
+
+@pytest.mark.parametrize("name,lens,q", [
+    ("deepseek_v2", [4096] * 48, 1), ("qwen3_30b_a3b", [4096, 300, 1024, 2048] * 32, 1),
+    ("rows_64", [3000, 500] * 24, 1), ("hybrid", [65536], 4)])
+def test_long_runs_give_the_same_bits(name, lens, q):
+    """Thousands of pages a call, where the warps of a CTA contend for shared memory and each
+    other's buffers: every one of ten calls gives the bits of the bf16 cache."""
+    f = Filled(name, lens, seed=3)
+    q_bits = f.query(q)
+    want = decode(f.dims, mla.mla_decode_attn, q_bits, f.bf16_cache(), f.table, f.lens)
+    for i in range(10):
+        got = decode(f.dims, mla.mla_decode_attn_q8, q_bits, f.cache, f.table, f.lens)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]), f"call {i}"
