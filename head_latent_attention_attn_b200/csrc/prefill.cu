@@ -60,7 +60,7 @@ constexpr uint32_t kQGroup = 3 * kBlk;
 constexpr uint32_t kSlotOff = 2 * kQGroup;       // K unrotated / V, 2 blocks each
 constexpr uint32_t kRopeOff = kSlotOff + kSlots * 2 * kBlk;
 constexpr uint32_t kMiscOff = kRopeOff + 2 * kBlk;
-constexpr uint32_t kBars = 4 + 2 * kSlots + 10 + 5;
+constexpr uint32_t kBars = 4 + 2 * kSlots + 10 + 6;
 constexpr uint32_t kInfoOff = kMiscOff + 16;     // [2] unit descriptions, 32 bytes each
 constexpr uint32_t kRespOff = kInfoOff + 64;     // answer of the launch control, 16 bytes
 constexpr uint32_t kBarOff = kRespOff + 16;
@@ -141,6 +141,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* info_full = o_free + 2;              // [2]
   uint64_t* info_empty = info_full + 2;          // [2]
   uint64_t* resp_full = info_empty + 2;
+  uint64_t* want = resp_full + 1;                // the producer is about to need a unit
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const WaitCtx wc{abort_flag, p.dev_error};
 
@@ -157,6 +158,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&info_empty[i], 10);             // producer, issuer, 8 row warps
     }
     mbar_init(resp_full, 1);
+    mbar_init(want, 1);
     for (int i = 0; i < kSlots; ++i) {
       mbar_init(&full[i], 1);
       mbar_init(&empty[i], 1);
@@ -248,7 +250,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (w.nt[0] > 0) load_q(0);
           if (n > 0) load_tile(0, false);
           if (w.nt[1] > 0) load_q(1);
+          // the next unit is asked for with the last tile: asked for earlier, a CTA would sit on
+          // a unit that an idle one could have begun
+          if (n == 0) mbar_arrive(want);
           for (int t = 0; ok && t < n; ++t) {
+            if (t == n - 1) mbar_arrive(want);
             load_tile(t, true);
             if (t + 1 < n) load_tile(t + 1, false);
           }
@@ -316,18 +322,28 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           umma_commit(&pv_done[g]);
         };
-        Unit w;
-        for (uint32_t k = 0; ok && next_unit(k, &w, false); ++k) {
+        Unit w, after;
+        bool have_after = false;                 // `after` holds the unit after w
+        bool begun = false;                      // group 0's first scores of w are issued
+        for (uint32_t k = 0; ok; ++k) {
+          if (have_after) {
+            w = after;
+            have_after = false;
+            if (w.h < 0) break;
+          } else if (!next_unit(k, &w, false)) {
+            break;
+          }
           const int n = w.tiles();
           if (n == 0) continue;
-          k_slot = wait_tile();
+          if (!begun) k_slot = wait_tile();
 #pragma unroll
           for (int g = 0; g < 2; ++g)
-            if (w.nt[g] > 0) {
+            if (w.nt[g] > 0 && !(g == 0 && begun)) {
               ok = ok && mbar_wait(&q_full[g], q_ph[g].next(), wc);
               tc_fence_after();
               if (ok) scores(g, w.nt[g] == 1);
             }
+          begun = false;
           if (ok) umma_commit(&empty[k_slot]);
           // The weights P_g(t) lie over S_g(t); the products with them are issued before the
           // scores S_g(t + 1) that overwrite both, and the tensor core works in order.
@@ -343,6 +359,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!have_k) k_slot = wait_tile();
                 have_k = true;
                 if (ok) scores(g, t + 2 == w.nt[g]);
+              }
+              // Group 0 is done with this unit: its first scores of the next one, if that has
+              // come in, go ahead of group 1's last product and keep its rows busy meanwhile.
+              if (g == 0 && ok && t + 1 == n) {
+                if (mbar_test_wait(&info_full[(k + 1) & 1], ((k + 1) >> 1) & 1)) {
+                  next_unit(k + 1, &after, false);
+                  have_after = true;
+                  if (after.h >= 0 && after.nt[0] > 0 &&
+                      mbar_test_wait(&full[ring.slot], ring.round & 1) &&
+                      mbar_test_wait(&q_full[0], q_ph[0].n & 1)) {
+                    q_ph[0].next();
+                    k_slot = wait_tile();
+                    if (ok) scores(0, after.nt[0] == 1);
+                    begun = true;
+                  }
+                }
               }
             }
             if (ok && t + 1 < n) umma_commit(&empty[k_slot]);
@@ -371,6 +403,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           mbar_arrive(&info_full[k & 1]);
           if (u < 0) break;
+          if (!mbar_wait(want, k & 1, wc)) break;
           mbar_arrive_expect_tx(resp_full, 16);
           try_cancel_cta(base + kRespOff, resp_full);
           // (this wait ends by itself: the answer is the hardware's)
