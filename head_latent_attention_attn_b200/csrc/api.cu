@@ -1065,6 +1065,12 @@ mla_status mla_prefill_attn(const mla_dims* dims, const void* q, const void* k_n
   // half of the 126 MB L2 for the keys and values of the heads in work
   p.head_block = int32_t(std::max<int64_t>(
       1, std::min<int64_t>(int64_t(H) * batch, (int64_t(64) << 20) / (int64_t(kv_len) * (dn + dv) * 2))));
+  // Clusters of CTAs share the tiles of a unit while they all fit on the device at once (128 of
+  // 148 SMs: clusters of eight stay inside a GPC) and each is left at least two tiles.
+  const int64_t units = int64_t(H) * batch * ((int64_t(q_len) + 255) / 256);
+  const int tiles = (kv_len + 127) / 128;
+  p.split = 1;
+  while (p.split < 8 && units * p.split * 2 <= 128 && tiles >= p.split * 2 * 2) p.split *= 2;
   p.scale_log2 = dims->softmax_scale * 1.4426950408889634f;
   return launch_prefill(p, as_stream(stream)) == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }

@@ -29,6 +29,9 @@
 // neighbouring units overlap, where a CTA per unit spent 10 of 46 us (causal 4096 rows) on its
 // start, its first loads and its last group's output.
 //
+// Few units (a short chunk over a long context) leave most SMs idle: then a cluster of up to eight
+// CTAs shares a unit's tiles (kSplit), and merges its parts through distributed shared memory.
+//
 // Softmax in the log2 domain with a reference maximum that moves only when a score exceeds it by
 // more than 8 (weights stay <= 256), so that O is rescaled rarely; the row itself then does it.
 #include <math.h>
@@ -68,13 +71,14 @@ constexpr uint32_t kSmem = kBarOff + 8 * kBars + 1024;   // + alignment slack
 static_assert(kSmem <= 232448, "shared memory of a CTA");
 
 // What a CTA works on: 256 query rows from row0 of head h of sequence b, which has L tokens and
-// ql query rows; group g's rows see nt[g] tiles. h < 0: no further unit.
+// ql query rows; group g's rows see nt[g] tiles from tile t0 on. h < 0: no further unit.
 struct Unit {
-  int row0, h, b, L, ql, nt[2];
+  int row0, h, b, L, ql, nt[2], t0;
   MLA_DEVICE int tiles() const { return max(nt[0], nt[1]); }
 };
 
-MLA_DEVICE Unit make_unit(const PrefillParams& p, int u) {
+// Unit u of the grid, or with split > 1 the part of its tiles that CTA `rank` of the cluster takes.
+MLA_DEVICE Unit make_unit(const PrefillParams& p, int u, int rank, int split) {
   // Units in blocks of head_block heads whose keys and values share L2; in a block the query
   // tiles with the most tokens first (a causal chunk's last rows), so that the last are short.
   const int heads = p.heads * p.batch, qts = (p.q_len + 2 * kRows - 1) / (2 * kRows);
@@ -99,6 +103,10 @@ MLA_DEVICE Unit make_unit(const PrefillParams& p, int u) {
         first >= w.ql ? 0 : p.causal ? max(0, min(w.L, w.L - w.ql + last + 1)) : w.L;
     w.nt[g] = (seen + kTok - 1) / kTok;
   }
+  const int n = w.tiles(), end = n * (rank + 1) / split;
+  w.t0 = n * rank / split;
+#pragma unroll
+  for (int g = 0; g < 2; ++g) w.nt[g] = max(0, min(w.nt[g], end) - w.t0);
   return w;
 }
 
@@ -108,6 +116,15 @@ struct Phase {
   MLA_DEVICE uint32_t next() { return n++ & 1u; }
   MLA_DEVICE uint32_t last() const { return (n - 1) & 1u; }
 };
+
+// A CTA's part of a unit for the cluster's merge, over Q, K and V: O as [group][column / 4][row],
+// then reference and sum as [group][row].
+MLA_DEVICE float4* stage_o(uint8_t* base, int g, int col4, int row) {
+  return reinterpret_cast<float4*>(base) + (g * 32 + col4) * kRows + row;
+}
+MLA_DEVICE float2* stage_ml(uint8_t* base, int g, int row) {
+  return reinterpret_cast<float2*>(base + 2 * 32 * kRows * 16) + g * kRows + row;
+}
 
 // Position in the ring of K and V slots.
 struct Ring {
@@ -123,6 +140,7 @@ struct Ring {
 
 }  // namespace
 
+template <bool kSplit>
 __global__ void __launch_bounds__(kThreads, 1)
     mla_prefill_kernel(const __grid_constant__ PrefillParams p) {
   extern __shared__ uint8_t smem_raw[];
@@ -194,6 +212,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     w->ql = src[4];
     w->nt[0] = src[5];
     w->nt[1] = src[6];
+    w->t0 = src[7];
     if (whole_warp) __syncwarp();
     if (!whole_warp || lane == 0) mbar_arrive(&info_empty[k & 1]);
     return w->h >= 0;
@@ -236,13 +255,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (v) {
               mbar_arrive_expect_tx(bar, uint32_t(vb) * kBlk);
               for (int i = 0; i < vb; ++i)
-                tma_load_4d(dst + i * kBlk, &p.tm_v, 64 * i, w.h, t * kTok, w.b, bar);
+                tma_load_4d(dst + i * kBlk, &p.tm_v, 64 * i, w.h, (w.t0 + t) * kTok, w.b, bar);
             } else {
               mbar_arrive_expect_tx(bar, uint32_t(nb + rope) * kBlk);
               for (int i = 0; i < nb; ++i)
-                tma_load_4d(dst + i * kBlk, &p.tm_k, 64 * i, w.h, t * kTok, w.b, bar);
+                tma_load_4d(dst + i * kBlk, &p.tm_k, 64 * i, w.h, (w.t0 + t) * kTok, w.b, bar);
               if (rope)
-                tma_load_4d(base + kRopeOff + (tile & 1) * kBlk, &p.tm_kr, 0, kg, t * kTok, w.b, bar);
+                tma_load_4d(base + kRopeOff + (tile & 1) * kBlk, &p.tm_kr, 0, kg, (w.t0 + t) * kTok,
+                            w.b, bar);
               ++tile;
             }
             ring.next();
@@ -385,10 +405,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == 2) {
       // ===================================== scheduler ====================================
       if (elect_one()) {
-        int u = int(blockIdx.x);
+        const int split = kSplit ? p.split : 1, rank = kSplit ? int(cluster_ctarank()) : 0;
+        int u = int(blockIdx.x) / split;
         for (uint32_t k = 0;; ++k) {
           Unit w;
-          if (u >= 0) w = make_unit(p, u);
+          if (u >= 0) w = make_unit(p, u, rank, split);
           else w.h = -1;
           if (k >= 2 && !mbar_wait(&info_empty[k & 1], ((k >> 1) - 1) & 1, wc)) break;
           int* dst = reinterpret_cast<int*>(base + kInfoOff + 32 * (k & 1));
@@ -400,9 +421,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             dst[4] = w.ql;
             dst[5] = w.nt[0];
             dst[6] = w.nt[1];
+            dst[7] = w.t0;
           }
           mbar_arrive(&info_full[k & 1]);
           if (u < 0) break;
+          if (kSplit) {                          // one unit a cluster
+            u = -1;
+            continue;
+          }
           if (!mbar_wait(want, k & 1, wc)) break;
           mbar_arrive_expect_tx(resp_full, 16);
           try_cancel_cta(base + kRespOff, resp_full);
@@ -430,7 +456,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     Ring v_ring;                                 // the K or V tile before the next V tile
     uint32_t tiles = 0;                          // of this group so far
     bool ok = true;
-    Unit w;
+    Unit w, staged;                              // kSplit: the unit whose part is in O
+    staged.h = -1;
+    float m_part = kRefInit, l_part = 0.0f;
     for (uint32_t k = 0; ok && next_unit(k, &w, true); ++k) {
       const int n = w.tiles(), ng = g == 0 ? w.nt[0] : w.nt[1];
       const int L = w.L, ql = w.ql;
@@ -452,7 +480,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int e = 0; e < kTok; e += 32) tmem_ld32(t_s + e, s + e);
         tmem_wait_ld();
-        const int t0 = j * kTok;
+        const int t0 = (w.t0 + j) * kTok;
         if (t0 + kTok - 1 > lim) {
 #pragma unroll
           for (int e = 0; e < kTok; ++e)
@@ -531,15 +559,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok) break;
       // ----------------------------------- epilogue --------------------------------------
-      const bool real = qi < ql;
-      const float inv = l != 0.0f ? 1.0f / l : 0.0f;          // NaN stays NaN
-      const int64_t row = (int64_t(w.b) * p.q_len + qi) * p.heads + w.h;
-      if (real) p.lse[row] = l != 0.0f ? (m + __log2f(l)) * kLn2 : -INFINITY;
       if (ng > 0) {
         ok = __all_sync(0xffffffffu, mbar_wait(&pv_done[g], (tiles - 1) & 1, wc));
         if (!ok) break;
         tc_fence_after();
       }
+      if constexpr (kSplit) {                    // the cluster's merge follows below
+        staged = w;
+        m_part = m;
+        l_part = l;
+        break;
+      }
+      const bool real = qi < ql;
+      const int64_t row = (int64_t(w.b) * p.q_len + qi) * p.heads + w.h;
+      const float inv = l != 0.0f ? 1.0f / l : 0.0f;          // NaN stays NaN
+      if (real) p.lse[row] = l != 0.0f ? (m + __log2f(l)) * kLn2 : -INFINITY;
       uint16_t* out = p.o + row * p.dv;
 #pragma unroll 1
       for (int e = 0; e < 64 * vb; e += 32) {
@@ -566,20 +600,102 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     // after a wait that ran out this CTA's rows stay unwritten; the error word tells
     tc_fence_before();
+    if constexpr (kSplit) {
+      // Unnormalised O, the reference and the sum into shared memory, once the products of both
+      // groups have read Q, K and V there (all eight warps come here, after an abort too).
+      named_bar_sync(1, 256);
+      if (staged.h >= 0) {
+        const bool any = (g == 0 ? staged.nt[0] : staged.nt[1]) > 0;
+        const int at = 32 * sp + lane;
+        *stage_ml(base, g, at) = make_float2(m_part, l_part);
+#pragma unroll 1
+        for (int e = 0; e < 64 * vb; e += 32) {
+          float o[32];
+          if (any) {
+            tmem_ld32(t_o + e, o);
+            tmem_wait_ld();
+          }
+#pragma unroll
+          for (int i = 0; i < 32; i += 4)
+            *stage_o(base, g, (e + i) / 4, at) =
+                any ? make_float4(o[i], o[i + 1], o[i + 2], o[i + 3])
+                    : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        }
+        tc_fence_before();
+      }
+      cluster_sync_all();                        // every CTA's part is in its shared memory
+      // This CTA merges its share of the columns of all rows: o = sum_i 2^(m_i - M) O_i / sum_i
+      // 2^(m_i - M) l_i over the cluster's CTAs, M = max m_i (a part without tokens has l_i = 0
+      // and the least m_i).
+      const int qi = staged.row0 + g * kRows + 32 * sp + lane, rl = 32 * sp + lane;
+      if (staged.h >= 0 && qi < staged.ql) {
+        const int s = p.split, rank = int(cluster_ctarank());
+        float m = kRefInit;
+        for (int i = 0; i < s; ++i)
+          m = fmaxf(m, ld_cluster_f32(map_to_rank(smem_u32(&stage_ml(base, g, rl)->x), i)));
+        float wgt[8], l = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          if (i >= s) break;
+          const uint32_t at = map_to_rank(smem_u32(stage_ml(base, g, rl)), i);
+          wgt[i] = ex2_approx(ld_cluster_f32(at) - m);
+          l += wgt[i] * ld_cluster_f32(at + 4);
+        }
+        const float inv = l != 0.0f ? 1.0f / l : 0.0f;        // NaN stays NaN
+        const int64_t row = (int64_t(staged.b) * p.q_len + qi) * p.heads + staged.h;
+        if (rank == 0) p.lse[row] = l != 0.0f ? (m + __log2f(l)) * kLn2 : -INFINITY;
+        const int cols = 64 * vb / s;            // 8 at least
+        for (int e = rank * cols; e < (rank + 1) * cols && e < p.dv; e += 8) {
+          float o[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            if (i >= s) break;
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+              const float4 v =
+                  ld_cluster_v4(map_to_rank(smem_u32(stage_o(base, g, e / 4 + q, rl)), i));
+              o[4 * q] += wgt[i] * v.x;
+              o[4 * q + 1] += wgt[i] * v.y;
+              o[4 * q + 2] += wgt[i] * v.z;
+              o[4 * q + 3] += wgt[i] * v.w;
+            }
+          }
+          uint32_t x[4];
+#pragma unroll
+          for (int y = 0; y < 4; ++y)
+            x[y] = inv == 0.0f ? 0u : cvt_bf16x2(o[2 * y] * inv, o[2 * y + 1] * inv);
+          *reinterpret_cast<uint4*>(p.o + row * p.dv + e) = make_uint4(x[0], x[1], x[2], x[3]);
+        }
+      }
+    }
+  }
+  if constexpr (kSplit) {
+    if (warp < 4) {
+      __syncwarp();
+      cluster_sync_all();
+    }
+    cluster_sync_all();                          // nobody leaves while its part may be read
   }
   tc_fence_before();
   __syncthreads();
   if (warp == 1) tmem_dealloc(tmem, 512);
 }
 
-cudaError_t launch_prefill(const PrefillParams& p, cudaStream_t stream) {
-  static const bool regs_ok = launched_with_regs(mla_prefill_kernel, kRegsLaunch);
+template <bool kSplit>
+static cudaError_t launch_prefill_t(const PrefillParams& p, unsigned units, cudaStream_t stream) {
+  static const bool regs_ok = launched_with_regs(mla_prefill_kernel<kSplit>, kRegsLaunch);
   if (!regs_ok) return cudaErrorInvalidDeviceFunction;
   const cudaError_t e = cudaFuncSetAttribute(
-      mla_prefill_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kSmem));
+      mla_prefill_kernel<kSplit>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kSmem));
   if (e != cudaSuccess) return e;
+  return launch_pdl(mla_prefill_kernel<kSplit>, dim3(units * p.split), dim3(kThreads), kSmem, stream,
+                    p.split, p);
+}
+
+cudaError_t launch_prefill(const PrefillParams& p, cudaStream_t stream) {
   const unsigned units = unsigned((p.q_len + 2 * kRows - 1) / (2 * kRows)) * p.heads * p.batch;
-  return launch_pdl(mla_prefill_kernel, dim3(units), dim3(kThreads), kSmem, stream, 1, p);
+  return p.split > 1 ? launch_prefill_t<true>(p, units, stream)
+                     : launch_prefill_t<false>(p, units, stream);
 }
 
 }  // namespace mla

@@ -78,7 +78,7 @@ def check(d, x, lens, q_lens, causal, o, lse, heads=None):
 
 
 # heads, groups, d_n, d_r, d_v
-LAYOUTS = {"mla": (4, 1, 128, 64, 128), "grouped": (8, 4, 128, 8, 128), "no_rope": (2, 1, 64, 0, 64),
+LAYOUTS = {"many": (96, 1, 64, 16, 64), "mla": (4, 1, 128, 64, 128), "grouped": (8, 4, 128, 8, 128), "no_rope": (2, 1, 64, 0, 64),
            "odd": (3, 3, 96, 24, 72), "tiny": (4, 1, 16, 8, 16), "wide_v": (2, 2, 40, 64, 128)}
 
 
@@ -87,7 +87,7 @@ def dims(name):
     return mla.make_dims(H, G, 64, dn, dr, dv, 64, 1.0 / np.sqrt(dn + dr))
 
 
-@pytest.mark.parametrize("name", sorted(LAYOUTS))
+@pytest.mark.parametrize("name", sorted(set(LAYOUTS) - {"many"}))
 @pytest.mark.parametrize("q,n,lens,q_lens,causal", [
     (1, 1, [1, 1], None, True),
     (1, 300, [300, 1], None, True),
@@ -108,6 +108,27 @@ def test_matches_the_formula(name, q, n, lens, q_lens, causal):
     check(d, x, lens, q_lens, causal, o, lse)
     o2, lse2, _ = run(d, x, lens, q_lens, causal, packed=dr % 8 == 0 and dr > 0)
     assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("name,q,n,lens,q_lens,causal,heads", [
+    ("mla", 40, 2300, [2300, 130, 1000], [40, 3, 40], True, None),      # clusters of eight
+    ("odd", 300, 1100, [1100, 300], [300, 130], True, None),            # of four, two row tiles
+    ("no_rope", 129, 2100, [2100], None, False, None),
+    ("many", 300, 700, [700, 650], [300, 257], True, [0, 37, 95]),      # more units than SMs
+    ("many", 700, 700, [700, 0, 129, 400], [700, 300, 129, 0], True, [1, 64, 94]),
+    ("many", 256, 1500, [1500, 1], None, False, [5, 90]),
+])
+def test_few_and_many_units(name, q, n, lens, q_lens, causal, heads):
+    """Few query rows over a long context (the CTAs of a cluster share the tiles of a unit), and
+    more units than SMs (CTAs take over units, of very different lengths)."""
+    H, G, dn, dr, dv = LAYOUTS[name]
+    x = make(len(lens), q, n, H, G, dn, dr, dv, seed=q + n)
+    o, lse, st = run(dims(name), x, lens, q_lens, causal)
+    assert st == mla.MLA_OK
+    check(dims(name), x, lens, q_lens, causal, o, lse, heads)
+    for _ in range(3):
+        o2, lse2, _ = run(dims(name), x, lens, q_lens, causal)
+        assert torch.equal(o, o2) and torch.equal(lse, lse2)
 
 
 def test_rows_that_see_nothing():
