@@ -61,15 +61,16 @@ namespace {
 
 constexpr int kThreads = 224;
 // Over the 8-bit cache (Q8) the roles are aligned groups of four warps, so that each can take
-// its own share of the registers (80 a thread at launch, 480 over the six groups): 0-2 TMA
-// producer, S^T issuer, PV issuer; 4-7 softmax and epilogue; 8-23 dequantise, two warps for
-// each 8-token group of a page, one per half of the column blocks.
+// its own share of the registers (128 a thread at launch, 512 over the four groups): 0-2 TMA
+// producer, S^T issuer, PV issuer; 4-7 softmax and epilogue; 8-15 dequantise, one 8-token group of
+// a page each. (Sixteen of them, with half of the column blocks each, measured slower: a warp has
+// some 100 instructions a page beside its conversions, which cost the softmax its issue slots.)
 template <bool Q8>
 constexpr int kPvWarp = Q8 ? 2 : 6;
 template <bool Q8>
 constexpr int kSmWarp0 = Q8 ? 4 : 2;                 // first of the four softmax warps
-constexpr int kDqWarp0 = 8, kDqWarps = 16;
-constexpr int kRegsLaunch = 80, kRegsIssue = 40, kRegsSoftmax = 216, kRegsDequant = 56;
+constexpr int kDqWarp0 = 8, kDqWarps = 8;
+constexpr int kRegsLaunch = 128, kRegsIssue = 72, kRegsSoftmax = 232, kRegsDequant = 104;
 // setmaxnreg may only lower a group's share by .dec and raise it by .inc
 static_assert(kRegsIssue <= kRegsLaunch && kRegsDequant <= kRegsLaunch &&
               kRegsSoftmax >= kRegsLaunch, "register shares");
@@ -419,10 +420,8 @@ __global__ void __launch_bounds__(kBlockThreads<Q8>, 1)
     // ============================== dequantising warps (Q8) ==============================
     if constexpr (Q8) reg_dec<kRegsDequant>();
     if (has_work) {
-      const int wi = warp - kDqWarp0, lb = p.r / kQ8Cols;
-      const int half = (lb + 1) / 2, blk0 = wi < 8 ? 0 : half;
-      dequant_pages<1>(p, cg, r0, r1, sched[0], sched[1], wi & 7, blk0, wi < 8 ? half : lb - half,
-                       blk0, slots, slot_bytes, full, empty, wc);
+      dequant_pages<kQ8MaxBlocks>(p, cg, r0, r1, sched[0], sched[1], warp - kDqWarp0, 0,
+                                  p.r / kQ8Cols, slots, slot_bytes, full, empty, wc);
     }
   } else {
   if constexpr (Q8) reg_inc<kRegsSoftmax>();

@@ -3,8 +3,7 @@
 //
 // A page's codes go from memory to the registers of the dequantising warps and from there, as
 // bf16, into the cache slot: no shared memory holds them in between, which the largest shapes
-// do not have. A warp converts groups of 8 tokens (lane: token lane / 4, 16 of the 64 columns) of
-// up to four column blocks; its loads of the next page are issued as soon as this page's codes have
+// do not have. A warp converts 8 tokens (lane: token lane / 4, 16 of the 64 columns); its loads of the next page are issued as soon as this page's codes have
 // left the registers, and the TMA producer brings pages into L2 ahead of them.
 #pragma once
 
@@ -14,7 +13,6 @@
 namespace mla {
 
 constexpr uint32_t kBlk8Bytes = kDecodeTok * 128;   // one 64 x 64 bf16 block of a slot
-constexpr int kDequantBlocks = 4;                   // column blocks of a warp at most
 constexpr int kDequantPrefetch = 3;                 // pages that the L2 prefetch runs ahead
 
 MLA_DEVICE void st_shared_v4(uint32_t saddr, const uint32_t* v) {
@@ -62,44 +60,35 @@ MLA_DEVICE void prefetch_pages(const DecodeParams& p, int cg, int r1, int upto, 
 }
 
 // All pages of tiles [r0, r1), whose first is of sequence b, which starts at tile s. This warp
-// converts the NG 8-token groups from grp0 on of the page's column blocks [blk0, blk0 + nb),
-// nb <= 4 (0: it only takes part in the slots' hand-over), into the slot's blocks dst0, dst0 + 1,
-// ... It waits for empty[slot] and arrives once on full[slot].
-template <int NG>
-MLA_DEVICE void dequant_pages(const DecodeParams& p, int cg, int r0, int r1, int b, int s, int grp0,
-                              int blk0, int nb, int dst0, uint8_t* slots, uint32_t slot_bytes,
+// converts 8-token group `grp` of the page's column blocks [blk0, blk0 + nb), nb <= NB, into the
+// slot's blocks 0, 1, ... It waits for empty[slot] and arrives once on full[slot].
+template <int NB>
+MLA_DEVICE void dequant_pages(const DecodeParams& p, int cg, int r0, int r1, int b, int s, int grp,
+                              int blk0, int nb, uint8_t* slots, uint32_t slot_bytes,
                               uint64_t* full, uint64_t* empty, const WaitCtx& wc) {
   const int lane = threadIdx.x & 31, part = lane & 3;
-  const int tok = 8 * grp0 + (lane >> 2);            // of the first group; + 8 g
+  const int tok = 8 * grp + (lane >> 2);
   const int R = p.D - p.r;
   const int64_t page_bytes = q8_page_bytes(p.r, R);
   const uint8_t* cache = static_cast<const uint8_t*>(p.cache_q8);
   const uint32_t code_off = uint32_t(blk0 * kQ8BlockBytes + tok * kQ8Cols + 16 * part);
   const uint32_t scale_off = uint32_t(q8_scales_offset(p.r, R) + tok * kQ8ScaleBytes);
-  // (tok + 8 g) % 8 does not depend on g: the swizzle is the same for all groups
-  const uint32_t st0 = smem_u32(slots) + dst0 * kBlk8Bytes + tok * 128 +
-                       (((2 * part) ^ (tok & 7)) << 4);
+  const uint32_t st0 = smem_u32(slots) + tok * 128 + (((2 * part) ^ (tok & 7)) << 4);
 
   PageWalk next(p, cg, r0, b, s);        // the tile to fetch; its page id is read a tile ahead
   int32_t page = next.page(p);
-  uint4 codes[NG][kDequantBlocks];
-  uint32_t scales[NG];                   // bytes of this warp's blocks
-  int live;                              // tokens of the context from `tok` on
+  uint4 codes[NB];
+  uint2 scales;
+  bool live;                             // a token of the context
   auto fetch = [&]() {
     if (page < 0 || page >= p.num_pages) page = 0;       // the TMA producer reports it
     const uint8_t* src = cache + page * page_bytes;
     // rows past the context are loaded too (they are part of the page) but not used
-    live = next.w.L - (next.t - next.w.s) * kDecodeTok - tok;
+    live = (next.t - next.w.s) * kDecodeTok + tok < next.w.L;
 #pragma unroll
-    for (int g = 0; g < NG; ++g) {
-#pragma unroll
-      for (int k = 0; k < kDequantBlocks; ++k)
-        if (k < nb)
-          codes[g][k] = ld_stream_v4(src + code_off + k * kQ8BlockBytes + g * 8 * kQ8Cols);
-      const uint2 sc =
-          *reinterpret_cast<const uint2*>(src + scale_off + g * 8 * kQ8ScaleBytes);
-      scales[g] = uint32_t((uint64_t(sc.y) << 32 | sc.x) >> (8 * blk0));
-    }
+    for (int k = 0; k < NB; ++k)
+      if (k < nb) codes[k] = ld_stream_v4(src + code_off + k * kQ8BlockBytes);
+    scales = *reinterpret_cast<const uint2*>(src + scale_off);
     next.next(p, cg, r1);
     if (next.t < r1) page = next.page(p);
   };
@@ -111,27 +100,22 @@ MLA_DEVICE void dequant_pages(const DecodeParams& p, int cg, int r0, int r1, int
         !__all_sync(0xffffffffu, mbar_wait(&empty[ring.slot], (ring.round - 1) & 1, wc)))
       break;
     const uint32_t at = st0 + ring.slot * slot_bytes;
-    if (__any_sync(0xffffffffu, live <= 8 * (NG - 1))) {
-      // the context ends in these groups: the rows past it, which may hold anything, become
-      // zeros (0-weight x garbage must not reach O)
+    if (!live) {
+      // rows past the context may hold anything: they become zeros (0-weight x garbage must
+      // not reach O)
+      scales = make_uint2(0, 0);
 #pragma unroll
-      for (int g = 0; g < NG; ++g)
-        if (live <= 8 * g) {
-          scales[g] = 0;
-#pragma unroll
-          for (int k = 0; k < kDequantBlocks; ++k) codes[g][k] = make_uint4(0, 0, 0, 0);
-        }
+      for (int k = 0; k < NB; ++k) codes[k] = make_uint4(0, 0, 0, 0);
     }
 #pragma unroll
-    for (int g = 0; g < NG; ++g) {
-#pragma unroll
-      for (int k = 0; k < kDequantBlocks; ++k) {
-        if (k >= nb) break;
-        uint32_t v[8];
-        q8_decode16(codes[g][k], q8_factor((scales[g] >> (8 * k)) & 0xFFu), v);
-        st_shared_v4(at + k * kBlk8Bytes + g * 1024, v);
-        st_shared_v4((at ^ 16u) + k * kBlk8Bytes + g * 1024, v + 4);
-      }
+    for (int k = 0; k < NB; ++k) {
+      if (k >= nb) break;
+      const uint32_t sc =
+          uint32_t((uint64_t(scales.y) << 32 | scales.x) >> (8 * (blk0 + k))) & 0xFFu;
+      uint32_t v[8];
+      q8_decode16(codes[k], q8_factor(sc), v);
+      st_shared_v4(at + k * kBlk8Bytes, v);
+      st_shared_v4((at ^ 16u) + k * kBlk8Bytes, v + 4);
     }
     // no proxy fence here: the UMMA issuer fences after it has waited for full[slot]
     __syncwarp();
