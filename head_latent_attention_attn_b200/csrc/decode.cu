@@ -77,6 +77,12 @@ static_assert(kRegsIssue <= kRegsLaunch && kRegsDequant <= kRegsLaunch &&
 static_assert(kRegsIssue + kRegsSoftmax + (kDqWarps / 4) * kRegsDequant <=
                   (2 + kDqWarps / 4) * kRegsLaunch,
               "the groups' registers exceed what the block is launched with");
+// Dequantising warps at work. Four with two groups each where the softmax of 64 columns is what a
+// page waits for and there is little to convert: r <= 256 (1M tokens, 64 rows, r 256: 193 us, 214
+// with eight); eight otherwise (64 rows, r 512: 187 us, 200 with four; 16 rows, r 256: 129 us, 147;
+// 32 rows, r 512: 436 us, 465).
+template <int NCOL>
+MLA_DEVICE int dequant_warps(int r) { return NCOL == 64 && r <= 4 * kQ8Cols ? 4 : kDqWarps; }
 template <bool Q8>
 constexpr int kBlockThreads = Q8 ? 32 * (kDqWarp0 + kDqWarps) : kThreads;
 constexpr int kBlkBytes = kDecodeTok * 128;   // one 64 x 64 bf16 block, 8 KB
@@ -228,7 +234,7 @@ __global__ void __launch_bounds__(kBlockThreads<Q8>, 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < p.nslot; ++s) {
-      mbar_init(&full[s], Q8 ? 1 + kDqWarps : 1);
+      mbar_init(&full[s], Q8 ? 1 + dequant_warps<NCOL>(p.r) : 1);
       mbar_init(&empty[s], 1);
     }
     mbar_init(q_full, 1);
@@ -420,8 +426,15 @@ __global__ void __launch_bounds__(kBlockThreads<Q8>, 1)
     // ============================== dequantising warps (Q8) ==============================
     if constexpr (Q8) reg_dec<kRegsDequant>();
     if (has_work) {
-      dequant_pages<kQ8MaxBlocks>(p, cg, r0, r1, sched[0], sched[1], warp - kDqWarp0, 0,
-                                  p.r / kQ8Cols, slots, slot_bytes, full, empty, wc);
+      const int wi = warp - kDqWarp0, lb = p.r / kQ8Cols;
+      if (dequant_warps<NCOL>(p.r) == 4) {
+        if (wi < 4)
+          dequant_pages<4, 2>(p, cg, r0, r1, sched[0], sched[1], wi, 0, lb, slots, slot_bytes, full,
+                              empty, wc);
+      } else {
+        dequant_pages<kQ8MaxBlocks, 1>(p, cg, r0, r1, sched[0], sched[1], wi, 0, lb, slots,
+                                       slot_bytes, full, empty, wc);
+      }
     }
   } else {
   if constexpr (Q8) reg_inc<kRegsSoftmax>();

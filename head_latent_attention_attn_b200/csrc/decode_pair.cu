@@ -507,8 +507,9 @@ __global__ void __launch_bounds__(kThreads<Q8>, 1)
     // ============================== dequantising warps (Q8) ==============================
     if constexpr (Q8) reg_dec<kRegsDequant>();
     if (has_work)
-      dequant_pages<kQ8MaxBlocks / 2>(p, cg, r0, r1, sched[0], sched[1], warp - kDqWarp0,
-                                      int(rank) * lb, lb, slots, lay.slot_bytes, full, empty, wc);
+      dequant_pages<kQ8MaxBlocks / 2, 1>(p, cg, r0, r1, sched[0], sched[1], warp - kDqWarp0,
+                                         int(rank) * lb, lb, slots, lay.slot_bytes, full, empty,
+                                         wc);
   } else if (has_work) {
     auto rows = [&](auto role_tag) {
     constexpr int role = decltype(role_tag)::value;   // 0 owner, 1 sender, 2 receiver

@@ -60,14 +60,14 @@ MLA_DEVICE void prefetch_pages(const DecodeParams& p, int cg, int r1, int upto, 
 }
 
 // All pages of tiles [r0, r1), whose first is of sequence b, which starts at tile s. This warp
-// converts 8-token group `grp` of the page's column blocks [blk0, blk0 + nb), nb <= NB, into the
-// slot's blocks 0, 1, ... It waits for empty[slot] and arrives once on full[slot].
-template <int NB>
+// converts the NG 8-token groups from NG * grp on of the page's column blocks [blk0, blk0 + nb),
+// nb <= NB, into the slot's blocks 0, 1, ... It waits for empty[slot] and arrives once on full[slot].
+template <int NB, int NG>
 MLA_DEVICE void dequant_pages(const DecodeParams& p, int cg, int r0, int r1, int b, int s, int grp,
                               int blk0, int nb, uint8_t* slots, uint32_t slot_bytes,
                               uint64_t* full, uint64_t* empty, const WaitCtx& wc) {
   const int lane = threadIdx.x & 31, part = lane & 3;
-  const int tok = 8 * grp + (lane >> 2);
+  const int tok = 8 * NG * grp + (lane >> 2);       // of the first group; + 8 g
   const int R = p.D - p.r;
   const int64_t page_bytes = q8_page_bytes(p.r, R);
   const uint8_t* cache = static_cast<const uint8_t*>(p.cache_q8);
@@ -77,18 +77,21 @@ MLA_DEVICE void dequant_pages(const DecodeParams& p, int cg, int r0, int r1, int
 
   PageWalk next(p, cg, r0, b, s);        // the tile to fetch; its page id is read a tile ahead
   int32_t page = next.page(p);
-  uint4 codes[NB];
-  uint2 scales;
-  bool live;                             // a token of the context
+  uint4 codes[NG][NB];
+  uint2 scales[NG];
+  int live;                              // tokens of the context from `tok` on
   auto fetch = [&]() {
     if (page < 0 || page >= p.num_pages) page = 0;       // the TMA producer reports it
     const uint8_t* src = cache + page * page_bytes;
     // rows past the context are loaded too (they are part of the page) but not used
-    live = (next.t - next.w.s) * kDecodeTok + tok < next.w.L;
+    live = next.w.L - (next.t - next.w.s) * kDecodeTok - tok;
 #pragma unroll
-    for (int k = 0; k < NB; ++k)
-      if (k < nb) codes[k] = ld_stream_v4(src + code_off + k * kQ8BlockBytes);
-    scales = *reinterpret_cast<const uint2*>(src + scale_off);
+    for (int g = 0; g < NG; ++g) {
+#pragma unroll
+      for (int k = 0; k < NB; ++k)
+        if (k < nb) codes[g][k] = ld_stream_v4(src + code_off + k * kQ8BlockBytes + g * 8 * kQ8Cols);
+      scales[g] = *reinterpret_cast<const uint2*>(src + scale_off + g * 8 * kQ8ScaleBytes);
+    }
     next.next(p, cg, r1);
     if (next.t < r1) page = next.page(p);
   };
@@ -100,22 +103,25 @@ MLA_DEVICE void dequant_pages(const DecodeParams& p, int cg, int r0, int r1, int
         !__all_sync(0xffffffffu, mbar_wait(&empty[ring.slot], (ring.round - 1) & 1, wc)))
       break;
     const uint32_t at = st0 + ring.slot * slot_bytes;
-    if (!live) {
-      // rows past the context may hold anything: they become zeros (0-weight x garbage must
-      // not reach O)
-      scales = make_uint2(0, 0);
 #pragma unroll
-      for (int k = 0; k < NB; ++k) codes[k] = make_uint4(0, 0, 0, 0);
-    }
+    for (int g = 0; g < NG; ++g) {
+      if (live <= 8 * g) {
+        // rows past the context may hold anything: they become zeros (0-weight x garbage must
+        // not reach O)
+        scales[g] = make_uint2(0, 0);
 #pragma unroll
-    for (int k = 0; k < NB; ++k) {
-      if (k >= nb) break;
-      const uint32_t sc =
-          uint32_t((uint64_t(scales.y) << 32 | scales.x) >> (8 * (blk0 + k))) & 0xFFu;
-      uint32_t v[8];
-      q8_decode16(codes[k], q8_factor(sc), v);
-      st_shared_v4(at + k * kBlk8Bytes, v);
-      st_shared_v4((at ^ 16u) + k * kBlk8Bytes, v + 4);
+        for (int k = 0; k < NB; ++k) codes[g][k] = make_uint4(0, 0, 0, 0);
+      }
+#pragma unroll
+      for (int k = 0; k < NB; ++k) {
+        if (k >= nb) break;
+        const uint32_t sc =
+            uint32_t((uint64_t(scales[g].y) << 32 | scales[g].x) >> (8 * (blk0 + k))) & 0xFFu;
+        uint32_t v[8];
+        q8_decode16(codes[g][k], q8_factor(sc), v);
+        st_shared_v4(at + k * kBlk8Bytes + g * 1024, v);
+        st_shared_v4((at ^ 16u) + k * kBlk8Bytes + g * 1024, v + 4);
+      }
     }
     // no proxy fence here: the UMMA issuer fences after it has waited for full[slot]
     __syncwarp();
