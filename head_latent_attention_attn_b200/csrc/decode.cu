@@ -78,7 +78,7 @@ static_assert(kRegsIssue + kRegsSoftmax + (kDqWarps / 4) * kRegsDequant <=
                   (2 + kDqWarps / 4) * kRegsLaunch,
               "the groups' registers exceed what the block is launched with");
 // Dequantising warps at work. Four with two groups each where the softmax of 64 columns is what a
-// page waits for and there is little to convert: r <= 256 (1M tokens, 64 rows, r 256: 193 us, 214
+// page waits for and there is little to convert: r <= 256 (1M tokens, 64 rows, r 256: 202 us, 214
 // with eight); eight otherwise (64 rows, r 512: 187 us, 200 with four; 16 rows, r 256: 129 us, 147;
 // 32 rows, r 512: 436 us, 465).
 template <int NCOL>
