@@ -867,7 +867,8 @@ mla_status mla_cache_read_q8(const mla_dims* dims, const void* cache, int64_t nu
   if (batch == 0 || n == 0) return MLA_OK;
   if (!cache || !block_table || !start_pos || !out) return MLA_ERR_INVALID_ARG;
   if (!aligned(cache, 16) || !aligned(out, 16)) return MLA_ERR_INVALID_ARG;
-  if (int64_t(batch) * ((int64_t(n) + 7) / 8) > int64_t(INT32_MAX) * 8) return MLA_ERR_UNSUPPORTED;
+  if (n > INT32_MAX - 64 || int64_t(batch) * ((int64_t(n) + 7) / 8) > int64_t(INT32_MAX) * 8)
+    return MLA_ERR_UNSUPPORTED;
   ReadQ8Params p{};
   p.cache = static_cast<const uint8_t*>(cache);
   p.block_table = block_table;

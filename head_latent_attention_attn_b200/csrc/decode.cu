@@ -700,8 +700,9 @@ template <int NCOL, bool Q8>
 static cudaError_t launch_decode_n(const DecodeParams& p, dim3 grid, size_t smem,
                                    cudaStream_t stream) {
   if (Q8) {
-    static const bool regs_ok = launched_with_regs(mla_decode_kernel<NCOL, Q8>, kRegsLaunch);
-    if (!regs_ok) return cudaErrorInvalidDeviceFunction;
+    static std::atomic<bool> known{false};
+    const cudaError_t e = check_launch_regs(mla_decode_kernel<NCOL, Q8>, kRegsLaunch, &known);
+    if (e != cudaSuccess) return e;
   }
   cudaError_t e = cudaFuncSetAttribute(mla_decode_kernel<NCOL, Q8>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));

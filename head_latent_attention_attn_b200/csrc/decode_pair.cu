@@ -964,8 +964,9 @@ template <bool Q8>
 static cudaError_t launch_decode_pair_t(const DecodeParams& p, dim3 grid, size_t smem,
                                         cudaStream_t stream) {
   if (Q8) {
-    static const bool regs_ok = launched_with_regs(mla_decode_pair_kernel<Q8>, kRegsLaunch);
-    if (!regs_ok) return cudaErrorInvalidDeviceFunction;
+    static std::atomic<bool> known{false};
+    const cudaError_t e = check_launch_regs(mla_decode_pair_kernel<Q8>, kRegsLaunch, &known);
+    if (e != cudaSuccess) return e;
   }
   cudaError_t e = cudaFuncSetAttribute(mla_decode_pair_kernel<Q8>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));

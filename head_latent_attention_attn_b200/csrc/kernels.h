@@ -5,6 +5,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
 #include <utility>
 
 namespace mla {
@@ -41,11 +42,20 @@ inline cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, s
 
 // Whether `kernel` is launched with exactly `regs` registers a thread: kernels that move registers
 // between their warps (setmaxnreg) add up shares of that number, and would wait forever for
-// registers that the block was not given. A property of the build; callers ask once.
+// registers that the block was not given. A property of the build, remembered in `known` once it
+// has been read.
 template <typename K>
-inline bool launched_with_regs(K* kernel, int regs) {
+inline cudaError_t check_launch_regs(K* kernel, int regs, std::atomic<bool>* known) {
+  if (known->load(std::memory_order_relaxed)) return cudaSuccess;
   cudaFuncAttributes a = {};
-  return cudaFuncGetAttributes(&a, kernel) == cudaSuccess && a.numRegs == regs;
+  const cudaError_t e = cudaFuncGetAttributes(&a, kernel);
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return e;
+  }
+  if (a.numRegs != regs) return cudaErrorInvalidDeviceFunction;
+  known->store(true, std::memory_order_relaxed);
+  return cudaSuccess;
 }
 
 // ---- mla_cache_append -------------------------------------------------------------------

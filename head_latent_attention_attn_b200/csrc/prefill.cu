@@ -683,9 +683,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 template <bool kSplit>
 static cudaError_t launch_prefill_t(const PrefillParams& p, unsigned units, cudaStream_t stream) {
-  static const bool regs_ok = launched_with_regs(mla_prefill_kernel<kSplit>, kRegsLaunch);
-  if (!regs_ok) return cudaErrorInvalidDeviceFunction;
-  const cudaError_t e = cudaFuncSetAttribute(
+  static std::atomic<bool> known{false};
+  cudaError_t e = check_launch_regs(mla_prefill_kernel<kSplit>, kRegsLaunch, &known);
+  if (e != cudaSuccess) return e;
+  e = cudaFuncSetAttribute(
       mla_prefill_kernel<kSplit>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kSmem));
   if (e != cudaSuccess) return e;
   return launch_pdl(mla_prefill_kernel<kSplit>, dim3(units * p.split), dim3(kThreads), kSmem, stream,

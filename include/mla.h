@@ -316,7 +316,8 @@ mla_status mla_decode_attn_q8(const mla_dims* dims, const void* q_ext, const voi
  * not used. A NaN or infinity in the value of a token t < L makes o NaN also for the rows of its
  * 128-row block that do not see t. A length out of range sets MLA_DEVERR_BOUNDS; that sequence
  * then sees nothing. P is rounded to bf16 as a tensor-core operand; scores, sums and o are fp32.
- * Requires d_n <= 128, d_v <= 128, d_r <= 64 and a multiple of 8 (MLA_ERR_UNSUPPORTED otherwise).
+ * Needs no workspace; q and kv_len are at least 1. Requires d_n <= 128, d_v <= 128, d_r <= 64 and a
+ * multiple of 8 (MLA_ERR_UNSUPPORTED otherwise).
  */
 mla_status mla_prefill_attn(const mla_dims* dims, const void* q, const void* k_nope,
                             int64_t k_token_stride, int64_t k_head_stride, const void* k_pe,

@@ -188,10 +188,13 @@ def test_bad_lengths_are_flagged():
         assert bool((seen == 0).all())
 
 
-def test_same_bits_again_in_a_graph_and_on_side_streams():
-    x = make(2, 300, 500, 8, 4, 128, 8, 128, seed=8)
-    lens, ql = [500, 280], [300, 280]
-    d = dims("grouped")
+@pytest.mark.parametrize("name", ["grouped", "many"])
+def test_same_bits_again_in_a_graph_and_on_side_streams(name):
+    """Few units (clusters) and more units than SMs (CTAs take over units)."""
+    H, G, dn, dr, dv = LAYOUTS[name]
+    x = make(2, 300, 600, H, G, dn, dr, dv, seed=8)
+    lens, ql = [600, 280], [300, 280]
+    d = dims(name)
     want = run(d, x, lens, ql)
     t = {k: bf(v) for k, v in x.items()}
     o, lse = torch.zeros_like(want[0]), torch.zeros_like(want[1])
