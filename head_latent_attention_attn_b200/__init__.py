@@ -38,7 +38,8 @@ C_SYMBOLS = ("mla_row_width", "mla_status_string", "mla_cache_append", "mla_abso
              "mla_kv_shared_decode_dims", "mla_kv_shared_query", "mla_kv_shared_output",
              "mla_down_kv_append", "mla_out_proj_workspace_size",
              "mla_out_proj", "mla_decode_step", "mla_q8_page_bytes", "mla_cache_append_q8",
-             "mla_cache_read_q8", "mla_decode_attn_q8", "mla_prefill_attn", "mla_decode_q8_workspace_size")
+             "mla_cache_read_q8", "mla_decode_attn_q8", "mla_prefill_attn",
+             "mla_decode_q8_workspace_size")
 
 
 class MlaError(RuntimeError):
@@ -454,7 +455,8 @@ def mla_decode_attn_q8(dims: MlaDims, q_ext, cache, block_table, seq_lens, max_s
 
 def _per_token(t, name: str, shape):
     """Token and head strides of a bf16 CUDA tensor [B, n, heads, width] whose last dim is
-    contiguous and whose batches follow one another. (The stride of a dim of size 1 says nothing.)"""
+    contiguous and whose batches follow one another. (The stride of a dim of size 1 says
+    nothing.)"""
     if not isinstance(t, torch.Tensor) or t.device.type != "cuda" or t.dtype != torch.bfloat16:
         raise MlaError(f"{name} must be a bfloat16 CUDA tensor", MLA_ERR_INVALID_ARG)
     if tuple(t.shape) != tuple(shape):

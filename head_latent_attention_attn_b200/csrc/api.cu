@@ -1064,8 +1064,9 @@ mla_status mla_prefill_attn(const mla_dims* dims, const void* q, const void* k_n
   p.dv = dv;
   p.causal = causal;
   // half of the 126 MB L2 for the keys and values of the heads in work
+  const int64_t head_bytes = int64_t(kv_len) * (dn + dv) * 2;
   p.head_block = int32_t(std::max<int64_t>(
-      1, std::min<int64_t>(int64_t(H) * batch, (int64_t(64) << 20) / (int64_t(kv_len) * (dn + dv) * 2))));
+      1, std::min<int64_t>(int64_t(H) * batch, (int64_t(64) << 20) / head_bytes)));
   // Clusters of CTAs share the tiles of a unit while they all fit on the device at once (128 of
   // 148 SMs: clusters of eight stay inside a GPC) and each is left at least two tiles.
   const int64_t units = int64_t(H) * batch * ((int64_t(q_len) + 255) / 256);

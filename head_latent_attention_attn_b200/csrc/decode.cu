@@ -269,159 +269,159 @@ __global__ void __launch_bounds__(kBlockThreads<Q8>, 1)
 
   const bool issuer = Q8 ? warp < 4 : warp < 2 || warp == kPvWarp<Q8>;
   if (issuer) {
-  if constexpr (Q8) reg_dec<kRegsIssue>();
-  if (warp == 0) {
-    // ===================================== TMA producer ==================================
-    if (has_work && elect_one()) {
-      prefetch_tensormap(Q8 ? &p.tm_rope : &p.tm_cache);
-      prefetch_tensormap(&p.tm_q);
-      if (blockIdx.x == 0) *p.range_len = per;
-      UnitWalk w{sched[0], sched[1]};
-      int jj = 0, pc = 0;
-      SlotRing ring(p.nslot);
-      bool ok = true;
-      PageWalk ahead{w};                  // the page to bring into L2 next (Q8 only)
-      if constexpr (Q8) ahead = PageWalk(p, cg, r0, sched[0], sched[1]);
-      for (; ok && w.s < r1; w.s += w.tiles, ++w.b, ++pc) {
-        w.load(p, cg);
-        p.unit_start[w.u] = w.s;   // same value from every CTA that touches the unit
-        const int tb = max(w.s, r0), te = min(w.s + w.tiles, r1);
-        if (pc > 0 && !mbar_wait(q_empty, (pc - 1) & 1, wc)) { ok = false; break; }
-        mbar_arrive_expect_tx(q_full, p.nblk * kQBlk);
-        for (int k = 0; k < p.nblk; ++k)
-          tma_load_3d(q_smem + k * kQBlk, &p.tm_q, k * 64, cg * NCOL, w.b, q_full);
-        const int32_t* bt = p.block_table + int64_t(w.b) * p.max_pages;
-        for (int t = tb; t < te; ++t, ++jj, ring.next()) {
-          const int slot = ring.slot;
-          // the page id is read before the wait, so its round trip overlaps it
-          int32_t page = bt[t - w.s];
-          if constexpr (Q8) prefetch_pages(p, cg, r1, t + kDequantPrefetch, ahead);
-          if (jj >= p.nslot && !mbar_wait(&empty[slot], (ring.round - 1) & 1, wc)) {
-            ok = false;
-            break;
-          }
-          MLA_TRACE_AT(0, jj);
-          if (page < 0 || page >= p.num_pages) {
-            if (p.dev_error) atomicOr(p.dev_error, MLA_DEVERR_BOUNDS);
-            page = 0;
-          }
-          uint8_t* sbase = slots + slot * slot_bytes;
-          uint64_t* fb = &full[slot];
-          if constexpr (Q8) {
-            // the rotated keys only; the latent blocks come from the dequantising warps
-            const int lb = p.r / kQ8Cols;
-            mbar_arrive_expect_tx(fb, uint32_t(p.nblk - lb) * kBlkBytes);
-            for (int k = lb; k < p.nblk; ++k)
-              tma_load_3d(sbase + k * kBlkBytes, &p.tm_rope, (k - lb) * 64, 0, page, fb);
-          } else {
-            mbar_arrive_expect_tx(fb, uint32_t(p.nblk) * kBlkBytes);
-            for (int k = 0; k < p.nblk; ++k)
-              tma_load_2d(sbase + k * kBlkBytes, &p.tm_cache, k * 64, page * kDecodeTok, fb);
-          }
-          MLA_TRACE_AT(8, jj);
-        }
-      }
-      // Drain: never leave while copies into this CTA's shared memory are in flight.
-      if (pc > 0) mbar_wait_bounded(q_full, (pc - 1) & 1, 200000000ull);
-      for (int j = (jj > p.nslot ? jj - p.nslot : 0); j < jj; ++j)
-        mbar_wait_bounded(&full[j % p.nslot], (j / p.nslot) & 1, 200000000ull);
-    }
-    __syncwarp();
-  } else if (warp == 1) {
-    // ================================ UMMA issuer for S^T ================================
-    // S^T(j) is issued once the whole page has landed. The PV products are issued by the
-    // softmax warps themselves, the moment P(j) is written.
-    if (has_work && elect_one()) {
-      const uint32_t idesc_s = make_idesc_bf16(64, NCOL, 0, 0);
-      const uint64_t a0 = make_sdesc(smem_u32(slots), 16, 1024, kSw128);
-      const uint64_t b0 = make_sdesc(smem_u32(q_smem), 16, 1024, kSw128);
-      const int nk16 = (p.D + 15) / 16;              // K steps over the row width
-      UnitWalk w{sched[0], sched[1]};
-      int jj = 0, pc = 0;
-      SlotRing ring(p.nslot);
-      bool ok = true;
-      for (; ok && w.s < r1; w.s += w.tiles, ++w.b, ++pc) {
-        w.load(p, cg);
-        const int tb = max(w.s, r0), te = min(w.s + w.tiles, r1);
-        if (!mbar_wait(q_full, pc & 1, wc)) { ok = false; break; }
-        for (int t = tb; ok && t < te; ++t, ++jj, ring.next()) {
-          const int slot = ring.slot;
-          const int sb = jj & 1;
-          if (jj >= 2 && !mbar_wait(&s_free[sb], ((jj - 2) >> 1) & 1, wc)) { ok = false; break; }
-          tc_fence_after();
-          const uint32_t soff = slot * slot_bytes;
-          if (!mbar_wait(&full[slot], ring.round & 1, wc)) { ok = false; break; }
-          if (Q8) fence_proxy_async_smem();   // the dequantising warps' stores, to the UMMAs
-          tc_fence_after();
-          MLA_TRACE_AT(9, jj);
-          // K steps of 16 columns over the row width; the descriptors step 32 bytes within
-          // a 64-column block and to the next block's start after its fourth step
-          {
-            const uint32_t dS = tmem + sb * NCOL;
-            uint64_t ad = a0 + (soff >> 4), bd = b0;
-            umma_bf16(dS, ad, bd, idesc_s, 0u);
-            for (int i = 1; i < nk16; ++i) {
-              const bool next_blk = (i & 3) == 0;
-              ad += next_blk ? uint64_t((kBlkBytes - 96) >> 4) : uint64_t(2);
-              bd += next_blk ? uint64_t((kQBlk - 96) >> 4) : uint64_t(2);
-              umma_bf16(dS, ad, bd, idesc_s, 1u);
+    if constexpr (Q8) reg_dec<kRegsIssue>();
+    if (warp == 0) {
+      // ===================================== TMA producer ==================================
+      if (has_work && elect_one()) {
+        prefetch_tensormap(Q8 ? &p.tm_rope : &p.tm_cache);
+        prefetch_tensormap(&p.tm_q);
+        if (blockIdx.x == 0) *p.range_len = per;
+        UnitWalk w{sched[0], sched[1]};
+        int jj = 0, pc = 0;
+        SlotRing ring(p.nslot);
+        bool ok = true;
+        PageWalk ahead{w};                  // the page to bring into L2 next (Q8 only)
+        if constexpr (Q8) ahead = PageWalk(p, cg, r0, sched[0], sched[1]);
+        for (; ok && w.s < r1; w.s += w.tiles, ++w.b, ++pc) {
+          w.load(p, cg);
+          p.unit_start[w.u] = w.s;   // same value from every CTA that touches the unit
+          const int tb = max(w.s, r0), te = min(w.s + w.tiles, r1);
+          if (pc > 0 && !mbar_wait(q_empty, (pc - 1) & 1, wc)) { ok = false; break; }
+          mbar_arrive_expect_tx(q_full, p.nblk * kQBlk);
+          for (int k = 0; k < p.nblk; ++k)
+            tma_load_3d(q_smem + k * kQBlk, &p.tm_q, k * 64, cg * NCOL, w.b, q_full);
+          const int32_t* bt = p.block_table + int64_t(w.b) * p.max_pages;
+          for (int t = tb; t < te; ++t, ++jj, ring.next()) {
+            const int slot = ring.slot;
+            // the page id is read before the wait, so its round trip overlaps it
+            int32_t page = bt[t - w.s];
+            if constexpr (Q8) prefetch_pages(p, cg, r1, t + kDequantPrefetch, ahead);
+            if (jj >= p.nslot && !mbar_wait(&empty[slot], (ring.round - 1) & 1, wc)) {
+              ok = false;
+              break;
             }
+            MLA_TRACE_AT(0, jj);
+            if (page < 0 || page >= p.num_pages) {
+              if (p.dev_error) atomicOr(p.dev_error, MLA_DEVERR_BOUNDS);
+              page = 0;
+            }
+            uint8_t* sbase = slots + slot * slot_bytes;
+            uint64_t* fb = &full[slot];
+            if constexpr (Q8) {
+              // the rotated keys only; the latent blocks come from the dequantising warps
+              const int lb = p.r / kQ8Cols;
+              mbar_arrive_expect_tx(fb, uint32_t(p.nblk - lb) * kBlkBytes);
+              for (int k = lb; k < p.nblk; ++k)
+                tma_load_3d(sbase + k * kBlkBytes, &p.tm_rope, (k - lb) * 64, 0, page, fb);
+            } else {
+              mbar_arrive_expect_tx(fb, uint32_t(p.nblk) * kBlkBytes);
+              for (int k = 0; k < p.nblk; ++k)
+                tma_load_2d(sbase + k * kBlkBytes, &p.tm_cache, k * 64, page * kDecodeTok, fb);
+            }
+            MLA_TRACE_AT(8, jj);
           }
-          MLA_TRACE_AT(1, jj);
-          umma_commit(&s_full[sb]);
-          MLA_TRACE_AT(2, jj);
-          if (t == te - 1) umma_commit(q_empty);   // this piece's Q is no longer read
+        }
+        // Drain: never leave while copies into this CTA's shared memory are in flight.
+        if (pc > 0) mbar_wait_bounded(q_full, (pc - 1) & 1, 200000000ull);
+        for (int j = (jj > p.nslot ? jj - p.nslot : 0); j < jj; ++j)
+          mbar_wait_bounded(&full[j % p.nslot], (j / p.nslot) & 1, 200000000ull);
+      }
+      __syncwarp();
+    } else if (warp == 1) {
+      // ================================ UMMA issuer for S^T ================================
+      // S^T(j) is issued once the whole page has landed. The PV products are issued by the
+      // softmax warps themselves, the moment P(j) is written.
+      if (has_work && elect_one()) {
+        const uint32_t idesc_s = make_idesc_bf16(64, NCOL, 0, 0);
+        const uint64_t a0 = make_sdesc(smem_u32(slots), 16, 1024, kSw128);
+        const uint64_t b0 = make_sdesc(smem_u32(q_smem), 16, 1024, kSw128);
+        const int nk16 = (p.D + 15) / 16;              // K steps over the row width
+        UnitWalk w{sched[0], sched[1]};
+        int jj = 0, pc = 0;
+        SlotRing ring(p.nslot);
+        bool ok = true;
+        for (; ok && w.s < r1; w.s += w.tiles, ++w.b, ++pc) {
+          w.load(p, cg);
+          const int tb = max(w.s, r0), te = min(w.s + w.tiles, r1);
+          if (!mbar_wait(q_full, pc & 1, wc)) { ok = false; break; }
+          for (int t = tb; ok && t < te; ++t, ++jj, ring.next()) {
+            const int slot = ring.slot;
+            const int sb = jj & 1;
+            if (jj >= 2 && !mbar_wait(&s_free[sb], ((jj - 2) >> 1) & 1, wc)) { ok = false; break; }
+            tc_fence_after();
+            const uint32_t soff = slot * slot_bytes;
+            if (!mbar_wait(&full[slot], ring.round & 1, wc)) { ok = false; break; }
+            if (Q8) fence_proxy_async_smem();   // the dequantising warps' stores, to the UMMAs
+            tc_fence_after();
+            MLA_TRACE_AT(9, jj);
+            // K steps of 16 columns over the row width; the descriptors step 32 bytes within
+            // a 64-column block and to the next block's start after its fourth step
+            {
+              const uint32_t dS = tmem + sb * NCOL;
+              uint64_t ad = a0 + (soff >> 4), bd = b0;
+              umma_bf16(dS, ad, bd, idesc_s, 0u);
+              for (int i = 1; i < nk16; ++i) {
+                const bool next_blk = (i & 3) == 0;
+                ad += next_blk ? uint64_t((kBlkBytes - 96) >> 4) : uint64_t(2);
+                bd += next_blk ? uint64_t((kQBlk - 96) >> 4) : uint64_t(2);
+                umma_bf16(dS, ad, bd, idesc_s, 1u);
+              }
+            }
+            MLA_TRACE_AT(1, jj);
+            umma_commit(&s_full[sb]);
+            MLA_TRACE_AT(2, jj);
+            if (t == te - 1) umma_commit(q_empty);   // this piece's Q is no longer read
+          }
         }
       }
-    }
-    __syncwarp();
-  } else if (warp == kPvWarp<Q8>) {
-    // =============================== UMMA issuer for PV ==================================
-    // O^T += C^T P^T for page j once the four softmax warps have written P^T(j) and zeroed
-    // the page's rows past the context; the first page of a piece overwrites O^T (the
-    // softmax warps read the previous piece's O^T before they arrive on P^T's barrier).
-    if (has_work && elect_one()) {
-      const uint32_t idesc_o = make_idesc_bf16(128, NCOL, 1, 1);
-      const uint64_t pa0 = make_sdesc(smem_u32(slots), kBlkBytes, 1024, kSw128);
-      const uint64_t pb0 = make_sdesc(smem_u32(pt), kPtBytes, 8 * NCOL * 2, pt_swizzle(NCOL));
-      UnitWalk w{sched[0], sched[1]};
-      int jj = 0;
-      SlotRing ring(p.nslot), pring(p.npt);
-      bool ok = true;
-      for (; ok && w.s < r1; w.s += w.tiles, ++w.b) {
-        w.load(p, cg);
-        const int tb = max(w.s, r0), te = min(w.s + w.tiles, r1);
-        for (int t = tb; t < te; ++t, ++jj, ring.next(), pring.next()) {
-          if (!mbar_wait(&p_full[pring.slot], pring.round & 1, wc)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          MLA_TRACE_AT(7, jj);
-          const bool first = (t == tb);
-          // K-step outer, latent chunk inner: consecutive MMAs feed different accumulators;
-          // descriptors stepped (16 tokens = 2 KB of C^T, 16 rows of P^T; 128 latent = 2
-          // blocks)
-          const uint64_t ad0 = pa0 + ((ring.slot * slot_bytes) >> 4);
-          uint64_t bd = pb0 + ((pring.slot * kPtBytes) >> 4);
+      __syncwarp();
+    } else if (warp == kPvWarp<Q8>) {
+      // =============================== UMMA issuer for PV ==================================
+      // O^T += C^T P^T for page j once the four softmax warps have written P^T(j) and zeroed
+      // the page's rows past the context; the first page of a piece overwrites O^T (the
+      // softmax warps read the previous piece's O^T before they arrive on P^T's barrier).
+      if (has_work && elect_one()) {
+        const uint32_t idesc_o = make_idesc_bf16(128, NCOL, 1, 1);
+        const uint64_t pa0 = make_sdesc(smem_u32(slots), kBlkBytes, 1024, kSw128);
+        const uint64_t pb0 = make_sdesc(smem_u32(pt), kPtBytes, 8 * NCOL * 2, pt_swizzle(NCOL));
+        UnitWalk w{sched[0], sched[1]};
+        int jj = 0;
+        SlotRing ring(p.nslot), pring(p.npt);
+        bool ok = true;
+        for (; ok && w.s < r1; w.s += w.tiles, ++w.b) {
+          w.load(p, cg);
+          const int tb = max(w.s, r0), te = min(w.s + w.tiles, r1);
+          for (int t = tb; t < te; ++t, ++jj, ring.next(), pring.next()) {
+            if (!mbar_wait(&p_full[pring.slot], pring.round & 1, wc)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            MLA_TRACE_AT(7, jj);
+            const bool first = (t == tb);
+            // K-step outer, latent chunk inner: consecutive MMAs feed different accumulators;
+            // descriptors stepped (16 tokens = 2 KB of C^T, 16 rows of P^T; 128 latent = 2
+            // blocks)
+            const uint64_t ad0 = pa0 + ((ring.slot * slot_bytes) >> 4);
+            uint64_t bd = pb0 + ((pring.slot * kPtBytes) >> 4);
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk) {
-            uint64_t ad = ad0 + uint64_t(kk * (2048 >> 4));
-            const uint32_t acc = (!first || kk > 0) ? 1u : 0u;
-            for (int c = 0; c < p.nch; ++c) {
-              umma_bf16(tmem + (2 + c) * NCOL, ad, bd, idesc_o, acc);
-              ad += uint64_t((2 * kBlkBytes) >> 4);
+            for (int kk = 0; kk < 4; ++kk) {
+              uint64_t ad = ad0 + uint64_t(kk * (2048 >> 4));
+              const uint32_t acc = (!first || kk > 0) ? 1u : 0u;
+              for (int c = 0; c < p.nch; ++c) {
+                umma_bf16(tmem + (2 + c) * NCOL, ad, bd, idesc_o, acc);
+                ad += uint64_t((2 * kBlkBytes) >> 4);
+              }
+              bd += uint64_t((16 * NCOL * 2) >> 4);
             }
-            bd += uint64_t((16 * NCOL * 2) >> 4);
+            umma_commit(&pv_done[jj & 1]);
+            umma_commit(&empty[ring.slot]);
+            MLA_TRACE_AT(3, jj);
           }
-          umma_commit(&pv_done[jj & 1]);
-          umma_commit(&empty[ring.slot]);
-          MLA_TRACE_AT(3, jj);
         }
       }
+      __syncwarp();
     }
-    __syncwarp();
-  }
   } else if (Q8 && warp >= kDqWarp0) {
     // ============================== dequantising warps (Q8) ==============================
     if constexpr (Q8) reg_dec<kRegsDequant>();
@@ -437,250 +437,251 @@ __global__ void __launch_bounds__(kBlockThreads<Q8>, 1)
       }
     }
   } else {
-  if constexpr (Q8) reg_inc<kRegsSoftmax>();
-  if (has_work) {
-    // ================================ softmax, epilogue ==================================
-    const int sp = warp & 3;                  // TMEM sub-partition this warp may access
-    const int wi = (sp + 2) & 3;              // index among the 4 softmax warps
-    const int tid = threadIdx.x - 32 * kSmWarp0<Q8>;   // 0..127
-    const uint32_t lane_base = uint32_t(sp * 32) << 16;
-    const int tok = 16 * sp + (lane & 15);    // token of this thread inside the tile
-    const int hf = lane >> 4;                 // which half of the columns
-    const int c0 = hf * HALF;                 // first column of this thread
-    const bool col_owner = (lane & 15) == 0;  // publishes its half-warp's column values
-    const float c_log2 = p.scale_log2;
+    if constexpr (Q8) reg_inc<kRegsSoftmax>();
+    if (has_work) {
+      // ================================ softmax, epilogue ==================================
+      const int sp = warp & 3;                  // TMEM sub-partition this warp may access
+      const int wi = (sp + 2) & 3;              // index among the 4 softmax warps
+      const int tid = threadIdx.x - 32 * kSmWarp0<Q8>;   // 0..127
+      const uint32_t lane_base = uint32_t(sp * 32) << 16;
+      const int tok = 16 * sp + (lane & 15);    // token of this thread inside the tile
+      const int hf = lane >> 4;                 // which half of the columns
+      const int c0 = hf * HALF;                 // first column of this thread
+      const bool col_owner = (lane & 15) == 0;  // publishes its half-warp's column values
+      const float c_log2 = p.scale_log2;
 
-    UnitWalk w{sched[0], sched[1]};
-    int jj = 0;
-    SlotRing ring(p.nslot), pring(p.npt);
-    for (; w.s < r1; w.s += w.tiles, ++w.b) {
-      w.load(p, cg);
-      const int tb = max(w.s, r0), te = min(w.s + w.tiles, r1);
-      const int L = w.L;
-      const int last_full = p.causal ? L - p.q_len : L - 1;  // last position every row sees
-      float m[HALF], l[HALF];
-#pragma unroll
-      for (int j = 0; j < HALF; ++j) {
-        m[j] = kRefInit;
-        l[j] = 0.0f;
-      }
-      for (int t = tb; t < te; ++t, ++jj, ring.next(), pring.next()) {
-        const int sb = jj & 1;
-        const uint32_t s_addr = tmem + lane_base + sb * NCOL;
-        const bool got = __all_sync(0xffffffffu, mbar_wait(&s_full[sb], (jj >> 1) & 1, wc));
-        if (tid == 0) MLA_TRACE_AT(4, jj);
-        const int tile_pos0 = (t - w.s) * kDecodeTok;
-        const int pos = tile_pos0 + tok;
-        const bool ragged = !got || tile_pos0 + kDecodeTok - 1 > last_full;
-        // tt = s * c - m: the scaled score against the current reference (in place)
-        float tt[HALF];
-        if (got) {
-          tc_fence_after();
-          tmem_ld_s<HALF>(s_addr, tt);
-          tmem_wait_ld();
-        }
-        if (ragged) {
-          // row (i, h) sees token pos iff pos < L and (causal) pos <= L - q + i
-#pragma unroll
-          for (int j = 0; j < HALF; ++j) {
-            const int qi = (cg * NCOL + c0 + j) / p.num_heads;
-            const bool vis = got && pos < L && (!p.causal || pos <= L - p.q_len + qi);
-            tt[j] = vis ? tt[j] : -INFINITY;
-          }
-        }
-        float tmax = -INFINITY;
+      UnitWalk w{sched[0], sched[1]};
+      int jj = 0;
+      SlotRing ring(p.nslot), pring(p.npt);
+      for (; w.s < r1; w.s += w.tiles, ++w.b) {
+        w.load(p, cg);
+        const int tb = max(w.s, r0), te = min(w.s + w.tiles, r1);
+        const int L = w.L;
+        const int last_full = p.causal ? L - p.q_len : L - 1;  // last position every row sees
+        float m[HALF], l[HALF];
 #pragma unroll
         for (int j = 0; j < HALF; ++j) {
-          tt[j] = fmaf(tt[j], c_log2, -m[j]);
-          tmax = fmaxf(tmax, tt[j]);
+          m[j] = kRefInit;
+          l[j] = 0.0f;
         }
-        const bool exceed = __any_sync(0xffffffffu, tmax > kLazyThreshold);
-        if (lane == 0) flags[(jj & 1) * 4 + wi] = exceed ? 1 : 0;
-        named_bar_sync(1, 128);
-        if (tid == 0) MLA_TRACE_AT(5, jj);
-        const int* fl = flags + (jj & 1) * 4;
-        if ((fl[0] | fl[1] | fl[2] | fl[3]) != 0) {
-          // Move the reference to the running column max of the scaled scores; the raw
-          // scores are read again from TMEM (the S buffer is released only below).
-          float s[HALF];
+        for (int t = tb; t < te; ++t, ++jj, ring.next(), pring.next()) {
+          const int sb = jj & 1;
+          const uint32_t s_addr = tmem + lane_base + sb * NCOL;
+          const bool got = __all_sync(0xffffffffu, mbar_wait(&s_full[sb], (jj >> 1) & 1, wc));
+          if (tid == 0) MLA_TRACE_AT(4, jj);
+          const int tile_pos0 = (t - w.s) * kDecodeTok;
+          const int pos = tile_pos0 + tok;
+          const bool ragged = !got || tile_pos0 + kDecodeTok - 1 > last_full;
+          // tt = s * c - m: the scaled score against the current reference (in place)
+          float tt[HALF];
           if (got) {
-            tmem_ld_s<HALF>(s_addr, s);
+            tc_fence_after();
+            tmem_ld_s<HALF>(s_addr, tt);
             tmem_wait_ld();
           }
+          if (ragged) {
+            // row (i, h) sees token pos iff pos < L and (causal) pos <= L - q + i
 #pragma unroll
-          for (int j = 0; j < HALF; ++j) {
-            if (ragged) {
+            for (int j = 0; j < HALF; ++j) {
               const int qi = (cg * NCOL + c0 + j) / p.num_heads;
               const bool vis = got && pos < L && (!p.causal || pos <= L - p.q_len + qi);
-              s[j] = vis ? s[j] : -INFINITY;
+              tt[j] = vis ? tt[j] : -INFINITY;
             }
-            float v = s[j] * c_log2;   // -inf stays -inf
-            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
-            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
-            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
-            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
-            if (col_owner) red[wi * 64 + c0 + j] = v;
           }
-          named_bar_sync(1, 128);
-          bool chg = false;
+          float tmax = -INFINITY;
 #pragma unroll
           for (int j = 0; j < HALF; ++j) {
-            const int n = c0 + j;
-            const float tm = fmaxf(fmaxf(red[n], red[64 + n]), fmaxf(red[128 + n], red[192 + n]));
-            const float mn = fmaxf(m[j], tm);
-            const float a = ex2_approx(m[j] - mn);   // 0 while m is still kRefInit
-            l[j] *= a;
-            m[j] = mn;
-            tt[j] = fmaf(s[j], c_log2, -mn);
-            chg |= a != 1.0f;
-            if (col_owner && wi == 0) alpha_s[n] = a;
+            tt[j] = fmaf(tt[j], c_log2, -m[j]);
+            tmax = fmaxf(tmax, tt[j]);
           }
-          if (col_owner && wi == 0) chg_flag[hf] = chg ? 1 : 0;
+          const bool exceed = __any_sync(0xffffffffu, tmax > kLazyThreshold);
+          if (lane == 0) flags[(jj & 1) * 4 + wi] = exceed ? 1 : 0;
           named_bar_sync(1, 128);
-          if (t > tb && (chg_flag[0] | chg_flag[1]) != 0) {
-            // O^T already holds this piece's earlier tiles: scale every column of the
-            // latent rows this thread owns (all threads see the same factors)
-            const bool okw = __all_sync(0xffffffffu,
-                                        mbar_wait(&pv_done[(jj - 1) & 1], ((jj - 1) >> 1) & 1, wc));
-            if (okw) {
-              tc_fence_after();
+          if (tid == 0) MLA_TRACE_AT(5, jj);
+          const int* fl = flags + (jj & 1) * 4;
+          if ((fl[0] | fl[1] | fl[2] | fl[3]) != 0) {
+            // Move the reference to the running column max of the scaled scores; the raw
+            // scores are read again from TMEM (the S buffer is released only below).
+            float s[HALF];
+            if (got) {
+              tmem_ld_s<HALF>(s_addr, s);
+              tmem_wait_ld();
+            }
+#pragma unroll
+            for (int j = 0; j < HALF; ++j) {
+              if (ragged) {
+                const int qi = (cg * NCOL + c0 + j) / p.num_heads;
+                const bool vis = got && pos < L && (!p.causal || pos <= L - p.q_len + qi);
+                s[j] = vis ? s[j] : -INFINITY;
+              }
+              float v = s[j] * c_log2;   // -inf stays -inf
+              v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+              v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+              v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
+              v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
+              if (col_owner) red[wi * 64 + c0 + j] = v;
+            }
+            named_bar_sync(1, 128);
+            bool chg = false;
+#pragma unroll
+            for (int j = 0; j < HALF; ++j) {
+              const int n = c0 + j;
+              const float tm = fmaxf(fmaxf(red[n], red[64 + n]), fmaxf(red[128 + n], red[192 + n]));
+              const float mn = fmaxf(m[j], tm);
+              const float a = ex2_approx(m[j] - mn);   // 0 while m is still kRefInit
+              l[j] *= a;
+              m[j] = mn;
+              tt[j] = fmaf(s[j], c_log2, -mn);
+              chg |= a != 1.0f;
+              if (col_owner && wi == 0) alpha_s[n] = a;
+            }
+            if (col_owner && wi == 0) chg_flag[hf] = chg ? 1 : 0;
+            named_bar_sync(1, 128);
+            if (t > tb && (chg_flag[0] | chg_flag[1]) != 0) {
+              // O^T already holds this piece's earlier tiles: scale every column of the
+              // latent rows this thread owns (all threads see the same factors)
+              const bool okw = __all_sync(
+                0xffffffffu, mbar_wait(&pv_done[(jj - 1) & 1], ((jj - 1) >> 1) & 1, wc));
+              if (okw) {
+                tc_fence_after();
 #pragma unroll 1
-              for (int n0 = 0; n0 < NCOL; n0 += 16) {
-                float a16[16];
+                for (int n0 = 0; n0 < NCOL; n0 += 16) {
+                  float a16[16];
 #pragma unroll
-                for (int n = 0; n < 16; ++n) a16[n] = alpha_s[n0 + n];
-                for (int c = 0; c < p.nch; ++c) {
-                  const uint32_t ta = tmem + lane_base + (2 + c) * NCOL + n0;
-                  float o[16];
-                  tmem_ld16(ta, o);
-                  tmem_wait_ld();
+                  for (int n = 0; n < 16; ++n) a16[n] = alpha_s[n0 + n];
+                  for (int c = 0; c < p.nch; ++c) {
+                    const uint32_t ta = tmem + lane_base + (2 + c) * NCOL + n0;
+                    float o[16];
+                    tmem_ld16(ta, o);
+                    tmem_wait_ld();
 #pragma unroll
-                  for (int n = 0; n < 16; ++n) o[n] *= a16[n];
-                  tmem_st16(ta, o);
+                    for (int n = 0; n < 16; ++n) o[n] *= a16[n];
+                    tmem_st16(ta, o);
+                  }
+                }
+                tmem_wait_st();
+              }
+            }
+          }
+
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&s_free[sb]);   // S buffer may be overwritten now
+
+          // unnormalised weights p = 2^(s*c - m) into this tile's P^T buffer (bf16)
+          if (jj >= p.npt) mbar_wait(&pv_done[(jj - p.npt) & 1], ((jj - p.npt) >> 1) & 1, wc);
+          if (tid == 0) MLA_TRACE_AT(6, jj);
+          uint32_t packed[HALF / 2];
+#pragma unroll
+          for (int j = 0; j < HALF; j += 2) {
+            const float p0 = ex2_approx(tt[j]);
+            const float p1 = ex2_approx(tt[j + 1]);
+            l[j] += p0;
+            l[j + 1] += p1;
+            packed[j / 2] = cvt_bf16x2(p0, p1);
+          }
+          const int slot = ring.slot;
+          const int pbuf = pring.slot;
+          {
+            uint8_t* buf = pt + pbuf * kPtBytes;
+            constexpr uint32_t kRowBytes = NCOL * 2;
+            constexpr uint32_t kChunkMask = kRowBytes / 16 - 1;
+#pragma unroll
+            for (int ch = 0; ch < HALF / 8; ++ch) {
+              const uint32_t off = tok * kRowBytes + (hf * (HALF / 8) + ch) * 16;
+              const uint32_t phys = off ^ (((off >> 7) & kChunkMask) << 4);
+              *reinterpret_cast<uint4*>(buf + phys) = make_uint4(
+                  packed[ch * 4 + 0], packed[ch * 4 + 1], packed[ch * 4 + 2], packed[ch * 4 + 3]);
+            }
+          }
+          // cache rows past the context may hold anything (even NaN): zero them so that
+          // 0-weight x garbage cannot reach O^T
+          if (!Q8 && pos >= L) {
+            uint8_t* sbase = slots + slot * slot_bytes;
+            for (int k = hf; k < 2 * p.nch; k += 2) {
+              uint4* rowp = reinterpret_cast<uint4*>(sbase + k * kBlkBytes + tok * 128);
+#pragma unroll
+              for (int ch = 0; ch < 8; ++ch) rowp[ch] = make_uint4(0, 0, 0, 0);
+            }
+          }
+          // P^T(j) and the zeroed rows are complete: hand the page to the PV issuer
+          fence_proxy_async_smem();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&p_full[pbuf]);
+        }
+
+        // ---------------------------- epilogue of this piece --------------------------------
+        const bool fin = __all_sync(0xffffffffu,
+                                    mbar_wait(&pv_done[(jj - 1) & 1], ((jj - 1) >> 1) & 1, wc));
+        tc_fence_after();
+#pragma unroll
+        for (int j = 0; j < HALF; ++j) {
+          float v = l[j];
+          v += __shfl_xor_sync(0xffffffffu, v, 8);
+          v += __shfl_xor_sync(0xffffffffu, v, 4);
+          v += __shfl_xor_sync(0xffffffffu, v, 2);
+          v += __shfl_xor_sync(0xffffffffu, v, 1);
+          l[j] = v;
+        }
+        named_bar_sync(1, 128);   // every earlier reader of red / mref_s is done
+        if (col_owner) {
+#pragma unroll
+          for (int j = 0; j < HALF; ++j) red[wi * 64 + c0 + j] = l[j];
+        }
+        if (col_owner && wi == 0) {
+#pragma unroll
+          for (int j = 0; j < HALF; ++j) mref_s[c0 + j] = m[j];
+        }
+        named_bar_sync(1, 128);
+        const bool aborted = __any_sync(0xffffffffu, !fin || *abort_flag != 0);
+        const bool whole = (tb == w.s) && (te == w.s + w.tiles);
+        const int cols_here = min(NCOL, p.qH - cg * NCOL);
+        const int64_t row0 = int64_t(w.b) * p.qH + int64_t(cg) * NCOL;   // first (b, i, h) row
+        const int pslot = piece_slot(vc, w.s, per, p.col_groups, cg);
+        if (tid < cols_here) {
+          const float sum = red[tid] + red[64 + tid] + red[128 + tid] + red[192 + tid];
+          const float lse =
+              (sum > 0.0f && !aborted) ? (mref_s[tid] + __log2f(sum)) * kLn2 : -INFINITY;
+          if (whole) p.lse[row0 + tid] = lse;
+          else p.part_lse[int64_t(pslot) * NCOL + tid] = lse;
+        }
+        // O^T: this thread owns latent row 128*c + 32*sp + lane of every chunk c
+#pragma unroll 1
+        for (int n0 = 0; n0 < NCOL; n0 += 16) {
+          float inv[16];
+#pragma unroll
+          for (int n = 0; n < 16; ++n) {
+            const int col = n0 + n;
+            const float sum = red[col] + red[64 + col] + red[128 + col] + red[192 + col];
+            inv[n] = sum > 0.0f ? 1.0f / sum : 0.0f;
+          }
+          for (int c = 0; c < p.nch; ++c) {
+            const int lat = 128 * c + 32 * sp + lane;
+            float o[16];
+            if (!aborted) {
+              tmem_ld16(tmem + lane_base + (2 + c) * NCOL + n0, o);
+              tmem_wait_ld();
+            } else {
+#pragma unroll
+              for (int n = 0; n < 16; ++n) o[n] = 0.0f;
+            }
+            if (lat < p.r) {
+#pragma unroll
+              for (int n = 0; n < 16; ++n) {
+                const int col = n0 + n;
+                if (col < cols_here) {
+                  const float v = o[n] * inv[n];
+                  if (whole) p.o_latent[(row0 + col) * p.r + lat] = cvt_bf16(v);
+                  else p.part_o[(int64_t(pslot) * NCOL + col) * p.r + lat] = cvt_bf16(v);
                 }
               }
-              tmem_wait_st();
             }
           }
         }
-
         tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&s_free[sb]);   // S buffer may be overwritten now
-
-        // unnormalised weights p = 2^(s*c - m) into this tile's P^T buffer (bf16)
-        if (jj >= p.npt) mbar_wait(&pv_done[(jj - p.npt) & 1], ((jj - p.npt) >> 1) & 1, wc);
-        if (tid == 0) MLA_TRACE_AT(6, jj);
-        uint32_t packed[HALF / 2];
-#pragma unroll
-        for (int j = 0; j < HALF; j += 2) {
-          const float p0 = ex2_approx(tt[j]);
-          const float p1 = ex2_approx(tt[j + 1]);
-          l[j] += p0;
-          l[j + 1] += p1;
-          packed[j / 2] = cvt_bf16x2(p0, p1);
-        }
-        const int slot = ring.slot;
-        const int pbuf = pring.slot;
-        {
-          uint8_t* buf = pt + pbuf * kPtBytes;
-          constexpr uint32_t kRowBytes = NCOL * 2;
-          constexpr uint32_t kChunkMask = kRowBytes / 16 - 1;
-#pragma unroll
-          for (int ch = 0; ch < HALF / 8; ++ch) {
-            const uint32_t off = tok * kRowBytes + (hf * (HALF / 8) + ch) * 16;
-            const uint32_t phys = off ^ (((off >> 7) & kChunkMask) << 4);
-            *reinterpret_cast<uint4*>(buf + phys) = make_uint4(
-                packed[ch * 4 + 0], packed[ch * 4 + 1], packed[ch * 4 + 2], packed[ch * 4 + 3]);
-          }
-        }
-        // cache rows past the context may hold anything (even NaN): zero them so that
-        // 0-weight x garbage cannot reach O^T
-        if (!Q8 && pos >= L) {
-          uint8_t* sbase = slots + slot * slot_bytes;
-          for (int k = hf; k < 2 * p.nch; k += 2) {
-            uint4* rowp = reinterpret_cast<uint4*>(sbase + k * kBlkBytes + tok * 128);
-#pragma unroll
-            for (int ch = 0; ch < 8; ++ch) rowp[ch] = make_uint4(0, 0, 0, 0);
-          }
-        }
-        // P^T(j) and the zeroed rows are complete: hand the page to the PV issuer
-        fence_proxy_async_smem();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[pbuf]);
       }
-
-      // ---------------------------- epilogue of this piece --------------------------------
-      const bool fin = __all_sync(0xffffffffu,
-                                  mbar_wait(&pv_done[(jj - 1) & 1], ((jj - 1) >> 1) & 1, wc));
-      tc_fence_after();
-#pragma unroll
-      for (int j = 0; j < HALF; ++j) {
-        float v = l[j];
-        v += __shfl_xor_sync(0xffffffffu, v, 8);
-        v += __shfl_xor_sync(0xffffffffu, v, 4);
-        v += __shfl_xor_sync(0xffffffffu, v, 2);
-        v += __shfl_xor_sync(0xffffffffu, v, 1);
-        l[j] = v;
-      }
-      named_bar_sync(1, 128);   // every earlier reader of red / mref_s is done
-      if (col_owner) {
-#pragma unroll
-        for (int j = 0; j < HALF; ++j) red[wi * 64 + c0 + j] = l[j];
-      }
-      if (col_owner && wi == 0) {
-#pragma unroll
-        for (int j = 0; j < HALF; ++j) mref_s[c0 + j] = m[j];
-      }
-      named_bar_sync(1, 128);
-      const bool aborted = __any_sync(0xffffffffu, !fin || *abort_flag != 0);
-      const bool whole = (tb == w.s) && (te == w.s + w.tiles);
-      const int cols_here = min(NCOL, p.qH - cg * NCOL);
-      const int64_t row0 = int64_t(w.b) * p.qH + int64_t(cg) * NCOL;   // first (b, i, h) row
-      const int pslot = piece_slot(vc, w.s, per, p.col_groups, cg);
-      if (tid < cols_here) {
-        const float sum = red[tid] + red[64 + tid] + red[128 + tid] + red[192 + tid];
-        const float lse = (sum > 0.0f && !aborted) ? (mref_s[tid] + __log2f(sum)) * kLn2 : -INFINITY;
-        if (whole) p.lse[row0 + tid] = lse;
-        else p.part_lse[int64_t(pslot) * NCOL + tid] = lse;
-      }
-      // O^T: this thread owns latent row 128*c + 32*sp + lane of every chunk c
-#pragma unroll 1
-      for (int n0 = 0; n0 < NCOL; n0 += 16) {
-        float inv[16];
-#pragma unroll
-        for (int n = 0; n < 16; ++n) {
-          const int col = n0 + n;
-          const float sum = red[col] + red[64 + col] + red[128 + col] + red[192 + col];
-          inv[n] = sum > 0.0f ? 1.0f / sum : 0.0f;
-        }
-        for (int c = 0; c < p.nch; ++c) {
-          const int lat = 128 * c + 32 * sp + lane;
-          float o[16];
-          if (!aborted) {
-            tmem_ld16(tmem + lane_base + (2 + c) * NCOL + n0, o);
-            tmem_wait_ld();
-          } else {
-#pragma unroll
-            for (int n = 0; n < 16; ++n) o[n] = 0.0f;
-          }
-          if (lat < p.r) {
-#pragma unroll
-            for (int n = 0; n < 16; ++n) {
-              const int col = n0 + n;
-              if (col < cols_here) {
-                const float v = o[n] * inv[n];
-                if (whole) p.o_latent[(row0 + col) * p.r + lat] = cvt_bf16(v);
-                else p.part_o[(int64_t(pslot) * NCOL + col) * p.r + lat] = cvt_bf16(v);
-              }
-            }
-          }
-        }
-      }
-      tc_fence_before();
     }
-  }
   }
 
   tc_fence_before();

@@ -359,150 +359,152 @@ __global__ void __launch_bounds__(kThreads<Q8>, 1)
 
   const bool issuer = warp < kRowWarp0<Q8>;
   if (issuer) {
-  if constexpr (Q8) reg_dec<kRegsIssue>();
-  if (warp == 0) {
-    // ===================================== TMA producer ==================================
-    if (has_work && elect_one()) {
-      if (!Q8) prefetch_tensormap(&p.tm_cache);
-      prefetch_tensormap(&p.tm_rope);
-      if (blockIdx.x == 0) *p.range_len = per;
-      UnitWalk w{sched[0], sched[1]};
-      int jj = 0;
-      SlotRing ring(p.nslot);
-      bool ok = true;
-      for (; ok && w.s < r1; w.s += w.tiles, ++w.b) {
-        w.load(p, cg);
-        if (rank == 0) p.unit_start[w.u] = w.s;   // same value from every cluster
-        const int tb = max(w.s, r0), te = min(w.s + w.tiles, r1);
-        const int32_t* bt = p.block_table + int64_t(w.b) * p.max_pages;
-        for (int t = tb; t < te; ++t, ++jj, ring.next()) {
-          const int slot = ring.slot;
-          // the page id is read before the wait, so its round trip overlaps it
-          int32_t page = bt[t - w.s];
-          if (jj >= p.nslot && !mbar_wait(&empty[slot], (ring.round - 1) & 1, wc)) {
-            ok = false;
-            break;
+    if constexpr (Q8) reg_dec<kRegsIssue>();
+    if (warp == 0) {
+      // ===================================== TMA producer ==================================
+      if (has_work && elect_one()) {
+        if (!Q8) prefetch_tensormap(&p.tm_cache);
+        prefetch_tensormap(&p.tm_rope);
+        if (blockIdx.x == 0) *p.range_len = per;
+        UnitWalk w{sched[0], sched[1]};
+        int jj = 0;
+        SlotRing ring(p.nslot);
+        bool ok = true;
+        for (; ok && w.s < r1; w.s += w.tiles, ++w.b) {
+          w.load(p, cg);
+          if (rank == 0) p.unit_start[w.u] = w.s;   // same value from every cluster
+          const int tb = max(w.s, r0), te = min(w.s + w.tiles, r1);
+          const int32_t* bt = p.block_table + int64_t(w.b) * p.max_pages;
+          for (int t = tb; t < te; ++t, ++jj, ring.next()) {
+            const int slot = ring.slot;
+            // the page id is read before the wait, so its round trip overlaps it
+            int32_t page = bt[t - w.s];
+            if (jj >= p.nslot && !mbar_wait(&empty[slot], (ring.round - 1) & 1, wc)) {
+              ok = false;
+              break;
+            }
+            if (page < 0 || page >= p.num_pages) {
+              if (p.dev_error) atomicOr(p.dev_error, MLA_DEVERR_BOUNDS);
+              page = 0;
+            }
+            uint8_t* sbase = slots + slot * lay.slot_bytes;
+            uint64_t* fb = &full[slot];
+            if constexpr (Q8) {
+              mbar_arrive_expect_tx(fb, rope_bytes);
+              tma_load_3d(sbase + lay.rope_off, &p.tm_rope, int(rank) * rh, 0, page, fb);
+            } else {
+              mbar_arrive_expect_tx(fb, uint32_t(lb) * kBlk + rope_bytes);
+              for (int k = 0; k < lb; ++k)
+                tma_load_2d(sbase + k * kBlk, &p.tm_cache, int(rank) * rhalf + k * 64,
+                            page * kDecodeTok, fb);
+              tma_load_2d(sbase + lay.rope_off, &p.tm_rope, r + int(rank) * rh, page * kDecodeTok,
+                          fb);
+            }
+            MLA_PTRACE(0, jj);
           }
-          if (page < 0 || page >= p.num_pages) {
-            if (p.dev_error) atomicOr(p.dev_error, MLA_DEVERR_BOUNDS);
-            page = 0;
+        }
+        // Drain: never leave while copies into this CTA's shared memory are in flight.
+        for (int j = (jj > p.nslot ? jj - p.nslot : 0); j < jj; ++j)
+          mbar_wait_bounded(&full[j % p.nslot], (j / p.nslot) & 1, 200000000ull);
+      }
+      __syncwarp();
+    } else if (warp == 1) {
+      // ============================ UMMA issuer for the partial S ==========================
+      // S of tile j goes to buffer j % 2: it waits for its page and for the readers of tile
+      // j - 2's scores (P has buffers of its own).
+      if (has_work && elect_one()) {
+        const uint32_t idesc_s = make_idesc_bf16(128, kDecodeTok, 0, 0);
+        const uint64_t b0 = make_sdesc(smem_u32(slots), 16, 1024, kSw128);
+        const uint64_t br0 =
+            make_sdesc(smem_u32(slots + lay.rope_off), 16, 8 * rh * 2, rope_swizzle(rh));
+        const uint64_t aq0 = make_sdesc(smem_u32(qrope), 16, 8 * rh * 2, rope_swizzle(rh));
+        const uint64_t aql0 = make_sdesc(smem_u32(qlat), 16, 1024, kSw128);
+        const int kt = 4 * (min(rhalf, kQTmem) / 64);   // latent K steps with A in TMEM
+        UnitWalk w{sched[0], sched[1]};
+        int jj = 0, pc = 0;
+        SlotRing ring(p.nslot);
+        bool ok = true;
+        for (; ok && w.s < r1; w.s += w.tiles, ++w.b, ++pc) {
+          w.load(p, cg);
+          const int tb = max(w.s, r0), te = min(w.s + w.tiles, r1);
+          if (!mbar_wait(q_full, pc & 1, wc)) { ok = false; break; }
+          tc_fence_after();
+          for (int t = tb; ok && t < te; ++t, ++jj, ring.next()) {
+            const int slot = ring.slot;
+            const int sb = jj & 1;
+            // every block of the tile landed, then the S buffer free
+            if (!mbar_wait(&full[slot], ring.round & 1, wc)) { ok = false; break; }
+            if (Q8) fence_proxy_async_smem();   // the dequantising warps' stores, to the UMMAs
+            MLA_PTRACE(1, jj);
+            if (jj >= 2 && !mbar_wait(&s_free[sb], ((jj - 2) >> 1) & 1, wc)) {
+              ok = false;
+              break;
+            }
+            MLA_PTRACE(9, jj);
+            tc_fence_after();
+            const uint32_t dS = tmem + kColS + 64 * sb;
+            const uint32_t soff = slot * lay.slot_bytes;
+            // latent K steps: A = Q from TMEM (8 columns per step) for the first kt steps and
+            // from shared memory after them; B steps 32 bytes within a 64-column block and to
+            // the next block after its fourth step; then the rotary steps
+            {
+              uint64_t bd = b0 + (soff >> 4);
+              umma_bf16_ts(dS, tmem + kColQ, bd, idesc_s, 0u);
+              for (int i = 1; i < kt; ++i) {
+                bd += (i & 3) == 0 ? uint64_t((kBlk - 96) >> 4) : uint64_t(2);
+                umma_bf16_ts(dS, tmem + kColQ + i * 8, bd, idesc_s, 1u);
+              }
+              uint64_t qd = aql0;
+              for (int i = kt; i < 4 * lb; ++i) {
+                bd += (i & 3) == 0 ? uint64_t((kBlk - 96) >> 4) : uint64_t(2);
+                if (i > kt)
+                  qd += (i & 3) == 0 ? uint64_t(((kPairRows * 128) - 96) >> 4) : uint64_t(2);
+                umma_bf16(dS, qd, bd, idesc_s, 1u);
+              }
+              uint64_t ad = aq0, rd = br0 + (soff >> 4);
+              for (int kk = 0; kk < rh / 16; ++kk, ad += 2, rd += 2)
+                umma_bf16(dS, ad, rd, idesc_s, 1u);
+            }
+            umma_commit(&s_full[sb]);
+            MLA_PTRACE(2, jj);
           }
-          uint8_t* sbase = slots + slot * lay.slot_bytes;
-          uint64_t* fb = &full[slot];
-          if constexpr (Q8) {
-            mbar_arrive_expect_tx(fb, rope_bytes);
-            tma_load_3d(sbase + lay.rope_off, &p.tm_rope, int(rank) * rh, 0, page, fb);
-          } else {
-            mbar_arrive_expect_tx(fb, uint32_t(lb) * kBlk + rope_bytes);
-            for (int k = 0; k < lb; ++k)
-              tma_load_2d(sbase + k * kBlk, &p.tm_cache, int(rank) * rhalf + k * 64,
-                          page * kDecodeTok, fb);
-            tma_load_2d(sbase + lay.rope_off, &p.tm_rope, r + int(rank) * rh, page * kDecodeTok,
-                        fb);
-          }
-          MLA_PTRACE(0, jj);
         }
       }
-      // Drain: never leave while copies into this CTA's shared memory are in flight.
-      for (int j = (jj > p.nslot ? jj - p.nslot : 0); j < jj; ++j)
-        mbar_wait_bounded(&full[j % p.nslot], (j / p.nslot) & 1, 200000000ull);
-    }
-    __syncwarp();
-  } else if (warp == 1) {
-    // ============================ UMMA issuer for the partial S ==========================
-    // S of tile j goes to buffer j % 2: it waits for its page and for the readers of tile
-    // j - 2's scores (P has buffers of its own).
-    if (has_work && elect_one()) {
-      const uint32_t idesc_s = make_idesc_bf16(128, kDecodeTok, 0, 0);
-      const uint64_t b0 = make_sdesc(smem_u32(slots), 16, 1024, kSw128);
-      const uint64_t br0 =
-          make_sdesc(smem_u32(slots + lay.rope_off), 16, 8 * rh * 2, rope_swizzle(rh));
-      const uint64_t aq0 = make_sdesc(smem_u32(qrope), 16, 8 * rh * 2, rope_swizzle(rh));
-      const uint64_t aql0 = make_sdesc(smem_u32(qlat), 16, 1024, kSw128);
-      const int kt = 4 * (min(rhalf, kQTmem) / 64);   // latent K steps with A in TMEM
-      UnitWalk w{sched[0], sched[1]};
-      int jj = 0, pc = 0;
-      SlotRing ring(p.nslot);
-      bool ok = true;
-      for (; ok && w.s < r1; w.s += w.tiles, ++w.b, ++pc) {
-        w.load(p, cg);
-        const int tb = max(w.s, r0), te = min(w.s + w.tiles, r1);
-        if (!mbar_wait(q_full, pc & 1, wc)) { ok = false; break; }
-        tc_fence_after();
-        for (int t = tb; ok && t < te; ++t, ++jj, ring.next()) {
-          const int slot = ring.slot;
-          const int sb = jj & 1;
-          // every block of the tile landed, then the S buffer free
-          if (!mbar_wait(&full[slot], ring.round & 1, wc)) { ok = false; break; }
-          if (Q8) fence_proxy_async_smem();   // the dequantising warps' stores, to the UMMAs
-          MLA_PTRACE(1, jj);
-          if (jj >= 2 && !mbar_wait(&s_free[sb], ((jj - 2) >> 1) & 1, wc)) {
-            ok = false;
-            break;
-          }
-          MLA_PTRACE(9, jj);
-          tc_fence_after();
-          const uint32_t dS = tmem + kColS + 64 * sb;
-          const uint32_t soff = slot * lay.slot_bytes;
-          // latent K steps: A = Q from TMEM (8 columns per step) for the first kt steps and
-          // from shared memory after them; B steps 32 bytes within a 64-column block and to
-          // the next block after its fourth step; then the rotary steps
-          {
-            uint64_t bd = b0 + (soff >> 4);
-            umma_bf16_ts(dS, tmem + kColQ, bd, idesc_s, 0u);
-            for (int i = 1; i < kt; ++i) {
-              bd += (i & 3) == 0 ? uint64_t((kBlk - 96) >> 4) : uint64_t(2);
-              umma_bf16_ts(dS, tmem + kColQ + i * 8, bd, idesc_s, 1u);
-            }
-            uint64_t qd = aql0;
-            for (int i = kt; i < 4 * lb; ++i) {
-              bd += (i & 3) == 0 ? uint64_t((kBlk - 96) >> 4) : uint64_t(2);
-              if (i > kt) qd += (i & 3) == 0 ? uint64_t(((kPairRows * 128) - 96) >> 4) : uint64_t(2);
-              umma_bf16(dS, qd, bd, idesc_s, 1u);
-            }
-            uint64_t ad = aq0, rd = br0 + (soff >> 4);
-            for (int kk = 0; kk < rh / 16; ++kk, ad += 2, rd += 2) umma_bf16(dS, ad, rd, idesc_s, 1u);
-          }
-          umma_commit(&s_full[sb]);
-          MLA_PTRACE(2, jj);
-        }
-      }
-    }
-    __syncwarp();
-  } else if (warp == kPvWarp) {
-    // ============================== UMMA issuer for O += P C ==============================
-    if (has_work && elect_one()) {
-      const uint32_t idesc_o = make_idesc_bf16(128, rhalf, 0, 1);
-      // B operand: the latent blocks of the slot read MN-major (latent contiguous)
-      const uint64_t pb0 = make_sdesc(smem_u32(slots), kBlk, 1024, kSw128);
-      UnitWalk w{sched[0], sched[1]};
-      int jj = 0;
-      SlotRing ring(p.nslot);
-      bool ok = true;
-      for (; ok && w.s < r1; w.s += w.tiles, ++w.b) {
-        w.load(p, cg);
-        const int tb = max(w.s, r0), te = min(w.s + w.tiles, r1);
-        for (int t = tb; t < te; ++t, ++jj, ring.next()) {
-          const int sb = jj & 1;
-          if (!mbar_wait(&p_full[sb], (jj >> 1) & 1, wc)) { ok = false; break; }
-          tc_fence_after();
-          // the first tile of a piece overwrites O: the previous piece's epilogue read O
-          // before its warps arrived on p_full for this tile
-          const bool first = (t == tb);
-          const uint32_t soff = ring.slot * lay.slot_bytes;
+      __syncwarp();
+    } else if (warp == kPvWarp) {
+      // ============================== UMMA issuer for O += P C ==============================
+      if (has_work && elect_one()) {
+        const uint32_t idesc_o = make_idesc_bf16(128, rhalf, 0, 1);
+        // B operand: the latent blocks of the slot read MN-major (latent contiguous)
+        const uint64_t pb0 = make_sdesc(smem_u32(slots), kBlk, 1024, kSw128);
+        UnitWalk w{sched[0], sched[1]};
+        int jj = 0;
+        SlotRing ring(p.nslot);
+        bool ok = true;
+        for (; ok && w.s < r1; w.s += w.tiles, ++w.b) {
+          w.load(p, cg);
+          const int tb = max(w.s, r0), te = min(w.s + w.tiles, r1);
+          for (int t = tb; t < te; ++t, ++jj, ring.next()) {
+            const int sb = jj & 1;
+            if (!mbar_wait(&p_full[sb], (jj >> 1) & 1, wc)) { ok = false; break; }
+            tc_fence_after();
+            // the first tile of a piece overwrites O: the previous piece's epilogue read O
+            // before its warps arrived on p_full for this tile
+            const bool first = (t == tb);
+            const uint32_t soff = ring.slot * lay.slot_bytes;
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            umma_bf16_ts(tmem + kColO, tmem + kColP + 32 * sb + kk * 8,
-                         pb0 + ((soff + kk * 2048) >> 4), idesc_o,
-                         (!first || kk > 0) ? 1u : 0u);
-          umma_commit(&pv_done[sb]);
-          umma_commit(&empty[ring.slot]);
-          MLA_PTRACE(8, jj);
+            for (int kk = 0; kk < 4; ++kk)
+              umma_bf16_ts(tmem + kColO, tmem + kColP + 32 * sb + kk * 8,
+                           pb0 + ((soff + kk * 2048) >> 4), idesc_o,
+                           (!first || kk > 0) ? 1u : 0u);
+            umma_commit(&pv_done[sb]);
+            umma_commit(&empty[ring.slot]);
+            MLA_PTRACE(8, jj);
+          }
         }
       }
+      __syncwarp();
     }
-    __syncwarp();
-  }
   } else if (Q8 && warp >= kDqWarp0) {
     // ============================== dequantising warps (Q8) ==============================
     if constexpr (Q8) reg_dec<kRegsDequant>();
@@ -512,110 +514,125 @@ __global__ void __launch_bounds__(kThreads<Q8>, 1)
                                          wc);
   } else if (has_work) {
     auto rows = [&](auto role_tag) {
-    constexpr int role = decltype(role_tag)::value;   // 0 owner, 1 sender, 2 receiver
-    // ==================================== the 128 rows ====================================
-    // Every row warp works on 16 TMEM lanes of its sub-partition with 16x32bx2 accesses:
-    // lanes i and i + 16 of the warp share row i and take tokens 0-31 and 32-63 (or the
-    // two 16-column halves of every 32 columns of O).
-    const int sp = warp & 3;                  // TMEM sub-partition this warp reaches
-    const int qt = lane >> 4;                 // token half of this thread
-    const int i16 = lane & 15;
-    // owners work on this CTA's rows, senders and receivers on the partner's
-    const uint32_t grp = uint32_t(32 * sp + 16 * int(role == 0 ? rank : peer));
-    const int n = int(grp) + i16;             // query row (TMEM lane)
-    const int m = 16 * sp + i16;              // row within its CTA's block of 64
-    const uint32_t trow = tmem + (grp << 16);
-    const int row = cg * kPairRows + n;       // row (i, h) of the sequence's q*H rows
-    const bool row_ok = row < p.qH;
-    const float c_log2 = p.scale_log2;
-    const bool vec_out = (reinterpret_cast<uintptr_t>(p.o_latent) & 15u) == 0;
-    const int rpitch = rh * 2;                // bytes per Q rotary row in shared memory
-    const bool tr = (sp == 0 && lane == 0);
-    (void)tr;
-    const uint32_t xs_s = smem_u32(xs), xp_s = smem_u32(xp);
-    const uint32_t xs_r = map_to_rank(xs_s, peer), xp_r = map_to_rank(xp_s, peer);
-    const uint32_t xs_full_r0 = map_to_rank(smem_u32(&xs_full[0]), peer);
-    const uint32_t xs_full_r1 = map_to_rank(smem_u32(&xs_full[1]), peer);
-    const uint32_t xs_free_r0 = map_to_rank(smem_u32(&xs_free[0]), peer);
-    const uint32_t xs_free_r1 = map_to_rank(smem_u32(&xs_free[1]), peer);
-    const uint32_t xp_full_r = map_to_rank(smem_u32(xp_full), peer);
-    const uint32_t xp_free_r = map_to_rank(smem_u32(xp_free), peer);
+      constexpr int role = decltype(role_tag)::value;   // 0 owner, 1 sender, 2 receiver
+      // ==================================== the 128 rows ====================================
+      // Every row warp works on 16 TMEM lanes of its sub-partition with 16x32bx2 accesses:
+      // lanes i and i + 16 of the warp share row i and take tokens 0-31 and 32-63 (or the
+      // two 16-column halves of every 32 columns of O).
+      const int sp = warp & 3;                  // TMEM sub-partition this warp reaches
+      const int qt = lane >> 4;                 // token half of this thread
+      const int i16 = lane & 15;
+      // owners work on this CTA's rows, senders and receivers on the partner's
+      const uint32_t grp = uint32_t(32 * sp + 16 * int(role == 0 ? rank : peer));
+      const int n = int(grp) + i16;             // query row (TMEM lane)
+      const int m = 16 * sp + i16;              // row within its CTA's block of 64
+      const uint32_t trow = tmem + (grp << 16);
+      const int row = cg * kPairRows + n;       // row (i, h) of the sequence's q*H rows
+      const bool row_ok = row < p.qH;
+      const float c_log2 = p.scale_log2;
+      const bool vec_out = (reinterpret_cast<uintptr_t>(p.o_latent) & 15u) == 0;
+      const int rpitch = rh * 2;                // bytes per Q rotary row in shared memory
+      const bool tr = (sp == 0 && lane == 0);
+      (void)tr;
+      const uint32_t xs_s = smem_u32(xs), xp_s = smem_u32(xp);
+      const uint32_t xs_r = map_to_rank(xs_s, peer), xp_r = map_to_rank(xp_s, peer);
+      const uint32_t xs_full_r0 = map_to_rank(smem_u32(&xs_full[0]), peer);
+      const uint32_t xs_full_r1 = map_to_rank(smem_u32(&xs_full[1]), peer);
+      const uint32_t xs_free_r0 = map_to_rank(smem_u32(&xs_free[0]), peer);
+      const uint32_t xs_free_r1 = map_to_rank(smem_u32(&xs_free[1]), peer);
+      const uint32_t xp_full_r = map_to_rank(smem_u32(xp_full), peer);
+      const uint32_t xp_free_r = map_to_rank(smem_u32(xp_free), peer);
 
-    // This CTA's half of Q row n: the latent half into TMEM (16-element chunks dealt
-    // alternately to the two threads of the row), the rotary half into shared memory;
-    // zero rows past q*H. Ends with this warp's arrival on q_full (owners and senders).
-    auto load_q = [&](int b) {
-      const uint16_t* q = p.q_ext + (int64_t(b) * p.qH + row) * p.D;
-      for (int c0 = 0; c0 < rhalf; c0 += 32) {
-        const uint16_t* src = q + int(rank) * rhalf + c0 + 16 * qt;
-        uint32_t v[8];
-        if (row_ok) {
-          const uint4 a = *reinterpret_cast<const uint4*>(src);
-          const uint4 bb = *reinterpret_cast<const uint4*>(src + 8);
-          v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-          v[4] = bb.x; v[5] = bb.y; v[6] = bb.z; v[7] = bb.w;
-        } else {
+      // This CTA's half of Q row n: the latent half into TMEM (16-element chunks dealt
+      // alternately to the two threads of the row), the rotary half into shared memory;
+      // zero rows past q*H. Ends with this warp's arrival on q_full (owners and senders).
+      auto load_q = [&](int b) {
+        const uint16_t* q = p.q_ext + (int64_t(b) * p.qH + row) * p.D;
+        for (int c0 = 0; c0 < rhalf; c0 += 32) {
+          const uint16_t* src = q + int(rank) * rhalf + c0 + 16 * qt;
+          uint32_t v[8];
+          if (row_ok) {
+            const uint4 a = *reinterpret_cast<const uint4*>(src);
+            const uint4 bb = *reinterpret_cast<const uint4*>(src + 8);
+            v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+            v[4] = bb.x; v[5] = bb.y; v[6] = bb.z; v[7] = bb.w;
+          } else {
 #pragma unroll
-          for (int k = 0; k < 8; ++k) v[k] = 0u;
+            for (int k = 0; k < 8; ++k) v[k] = 0u;
+          }
+          if (c0 < kQTmem) tm_st_x8_s8(trow + kColQ + c0 / 2, v);
+          else store_qlat(qlat, n, c0 + 16 * qt - kQTmem, v);
         }
-        if (c0 < kQTmem) tm_st_x8_s8(trow + kColQ + c0 / 2, v);
-        else store_qlat(qlat, n, c0 + 16 * qt - kQTmem, v);
-      }
-      for (int c = qt; c < rh / 8; c += 2) {
-        const uint4 v = row_ok ? *reinterpret_cast<const uint4*>(q + r + int(rank) * rh + 8 * c)
-                               : make_uint4(0, 0, 0, 0);
-        *reinterpret_cast<uint4*>(qrope + swizzled_chunk(n, c, rpitch)) = v;
-      }
-      tmem_wait_st();
-      fence_proxy_async_smem();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(q_full);
-    };
+        for (int c = qt; c < rh / 8; c += 2) {
+          const uint4 v = row_ok ? *reinterpret_cast<const uint4*>(q + r + int(rank) * rh + 8 * c)
+                                 : make_uint4(0, 0, 0, 0);
+          *reinterpret_cast<uint4*>(qrope + swizzled_chunk(n, c, rpitch)) = v;
+        }
+        tmem_wait_st();
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(q_full);
+      };
 
-    // O rows of this warp times alpha (16 of every 32 columns per thread), once PV(jj - 1)
-    // has landed in O.
-    auto rescale_o = [&](int jj, float alpha) {
-      const bool pv_ok =
-          __all_sync(0xffffffffu, mbar_wait(&pv_done[(jj - 1) & 1], ((jj - 1) >> 1) & 1, wc));
-      tc_fence_after();
-      if (!pv_ok) return;
-      for (int c0 = 0; c0 < rhalf; c0 += 32) {
-        float o[16];
-        tm_ld_x16_s16(trow + kColO + c0, o);
-        tmem_wait_ld();
-#pragma unroll
-        for (int c = 0; c < 16; ++c) o[c] *= alpha;
-        tm_st_x16_s16(trow + kColO + c0, reinterpret_cast<const uint32_t*>(o));
-      }
-    };
-
-    // O rows of this warp divided by the row sum lt, to the outputs of piece (w, tb, te)
-    // whose last tile is jl: bf16 o_latent when the piece is the whole unit, else the bf16 partial part_o.
-    auto write_o = [&](const UnitWalk& w, int tb, int te, int jl, float lt, bool* aborted_out) {
-      const bool fin = __all_sync(0xffffffffu, mbar_wait(&pv_done[jl & 1], (jl >> 1) & 1, wc));
-      tc_fence_after();
-      const bool aborted = __any_sync(0xffffffffu, !fin || *abort_flag != 0);
-      *aborted_out = aborted;
-      const bool whole = (tb == w.s) && (te == w.s + w.tiles);
-      const int64_t grow = int64_t(w.b) * p.qH + row;   // global (b, i, h) row
-      const int pslot = piece_slot(vc, w.s, per, p.col_groups, cg);
-      const float inv = (lt > 0.0f && !aborted) ? 1.0f / lt : 0.0f;
-      const int64_t lat0 = int64_t(rank) * rhalf + 16 * qt;   // this thread's 16 of every 32
-      for (int c0 = 0; c0 < rhalf; c0 += 32) {
-        float o[16];
-        if (!aborted) {
+      // O rows of this warp times alpha (16 of every 32 columns per thread), once PV(jj - 1)
+      // has landed in O.
+      auto rescale_o = [&](int jj, float alpha) {
+        const bool pv_ok =
+            __all_sync(0xffffffffu, mbar_wait(&pv_done[(jj - 1) & 1], ((jj - 1) >> 1) & 1, wc));
+        tc_fence_after();
+        if (!pv_ok) return;
+        for (int c0 = 0; c0 < rhalf; c0 += 32) {
+          float o[16];
           tm_ld_x16_s16(trow + kColO + c0, o);
           tmem_wait_ld();
-        } else {
 #pragma unroll
-          for (int c = 0; c < 16; ++c) o[c] = 0.0f;
+          for (int c = 0; c < 16; ++c) o[c] *= alpha;
+          tm_st_x16_s16(trow + kColO + c0, reinterpret_cast<const uint32_t*>(o));
         }
-        if (!row_ok) {
-          // padding row past q*H: nothing to write
-        } else if (whole) {
-          uint16_t* dst = p.o_latent + grow * r + lat0 + c0;
-          if (vec_out) {
+      };
+
+      // O rows of this warp divided by the row sum lt, to the outputs of piece (w, tb, te)
+      // whose last tile is jl: bf16 o_latent when the piece is the whole unit, else the bf16
+      // partial part_o.
+      auto write_o = [&](const UnitWalk& w, int tb, int te, int jl, float lt, bool* aborted_out) {
+        const bool fin = __all_sync(0xffffffffu, mbar_wait(&pv_done[jl & 1], (jl >> 1) & 1, wc));
+        tc_fence_after();
+        const bool aborted = __any_sync(0xffffffffu, !fin || *abort_flag != 0);
+        *aborted_out = aborted;
+        const bool whole = (tb == w.s) && (te == w.s + w.tiles);
+        const int64_t grow = int64_t(w.b) * p.qH + row;   // global (b, i, h) row
+        const int pslot = piece_slot(vc, w.s, per, p.col_groups, cg);
+        const float inv = (lt > 0.0f && !aborted) ? 1.0f / lt : 0.0f;
+        const int64_t lat0 = int64_t(rank) * rhalf + 16 * qt;   // this thread's 16 of every 32
+        for (int c0 = 0; c0 < rhalf; c0 += 32) {
+          float o[16];
+          if (!aborted) {
+            tm_ld_x16_s16(trow + kColO + c0, o);
+            tmem_wait_ld();
+          } else {
+#pragma unroll
+            for (int c = 0; c < 16; ++c) o[c] = 0.0f;
+          }
+          if (!row_ok) {
+            // padding row past q*H: nothing to write
+          } else if (whole) {
+            uint16_t* dst = p.o_latent + grow * r + lat0 + c0;
+            if (vec_out) {
+#pragma unroll
+              for (int c = 0; c < 16; c += 8)
+                *reinterpret_cast<uint4*>(dst + c) =
+                    make_uint4(cvt_bf16x2(o[c] * inv, o[c + 1] * inv),
+                               cvt_bf16x2(o[c + 2] * inv, o[c + 3] * inv),
+                               cvt_bf16x2(o[c + 4] * inv, o[c + 5] * inv),
+                               cvt_bf16x2(o[c + 6] * inv, o[c + 7] * inv));
+            } else {
+#pragma unroll
+              for (int c = 0; c < 16; ++c) dst[c] = f32_to_bf16_rne(o[c] * inv);
+            }
+          } else {
+            // bf16 partial (16-byte aligned: r % 8 == 0 and lat0 + c0 a multiple of 16)
+            uint16_t* dst = p.part_o + (int64_t(pslot) * kPairRows + n) * r + lat0 + c0;
 #pragma unroll
             for (int c = 0; c < 16; c += 8)
               *reinterpret_cast<uint4*>(dst + c) =
@@ -623,283 +640,270 @@ __global__ void __launch_bounds__(kThreads<Q8>, 1)
                              cvt_bf16x2(o[c + 2] * inv, o[c + 3] * inv),
                              cvt_bf16x2(o[c + 4] * inv, o[c + 5] * inv),
                              cvt_bf16x2(o[c + 6] * inv, o[c + 7] * inv));
-          } else {
-#pragma unroll
-            for (int c = 0; c < 16; ++c) dst[c] = f32_to_bf16_rne(o[c] * inv);
           }
-        } else {
-          // bf16 partial (16-byte aligned: r % 8 == 0 and lat0 + c0 a multiple of 16)
-          uint16_t* dst = p.part_o + (int64_t(pslot) * kPairRows + n) * r + lat0 + c0;
-#pragma unroll
-          for (int c = 0; c < 16; c += 8)
-            *reinterpret_cast<uint4*>(dst + c) =
-                make_uint4(cvt_bf16x2(o[c] * inv, o[c + 1] * inv),
-                           cvt_bf16x2(o[c + 2] * inv, o[c + 3] * inv),
-                           cvt_bf16x2(o[c + 4] * inv, o[c + 5] * inv),
-                           cvt_bf16x2(o[c + 6] * inv, o[c + 7] * inv));
         }
-      }
-      tc_fence_before();
-    };
+        tc_fence_before();
+      };
 
-    if constexpr (role == 0) {
-      // ------------- owner: this CTA's 16 rows of sub-partition sp; softmax and P ---------
-      const int qi = row / p.num_heads;
-      load_q(sched[0]);
-      UnitWalk w{sched[0], sched[1]};
-      w.load(p, cg);
-      int jj = 0;
-      SlotRing ring(p.nslot);
-      while (true) {
-        const int tb = max(w.s, r0), te = min(w.s + w.tiles, r1);
-        const int L = w.L;
-        // last position row n sees (causal: L - q + i); rows past q*H see L - 1
-        const int lim = min(L - 1, p.causal ? L - p.q_len + qi : L - 1);
-        float mref = kRefInit, l = 0.0f, lt = 0.0f;   // the same in both threads of a row
-        for (int t = tb; t < te; ++t, ++jj, ring.next()) {
-          const int sb = jj & 1;                 // S buffer and partial buffer of this tile
-          const int slot = ring.slot;
-          const int tile_pos0 = (t - w.s) * kDecodeTok;
-          const int pos0 = tile_pos0 + qt * kHalfTok;   // first token of this thread's half
-          // ---- own partial scores ----
-          float s[kHalfTok];
-          const bool got = __all_sync(0xffffffffu, mbar_wait(&s_full[sb], (jj >> 1) & 1, wc));
-          tc_fence_after();
-          if (got) {
-            tm_ld_x32_s32(trow + kColS + 64 * sb, s);
-            tmem_wait_ld();
-          } else {
-#pragma unroll
-            for (int c = 0; c < kHalfTok; ++c) s[c] = 0.0f;
-          }
-          if (tr) MLA_PTRACE(10, jj);
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&s_free[sb]);
-          // S of the piece's last tile is complete: the next piece's Q may replace this one
-          if (t == te - 1 && w.s + w.tiles < r1) load_q(w.b + 1);
-          // ---- plus the partner's partial ----
-          const bool rcv =
-              __all_sync(0xffffffffu, mbar_wait_cluster(&xs_full[sb], (jj >> 1) & 1, wc));
-          if (tr) MLA_PTRACE(5, jj);
-          uint32_t read_words = 0;
-          {
-            const uint32_t src = xs_s + sb * kXsBytes;
-            uint32_t wb[kPackWords];
-#pragma unroll
-            for (int c = 0; c < kPackWords / 4; ++c) {
-              const uint4 v = ld_shared_v4(src + xs_offset(sp, lane, c));
-              wb[4 * c] = v.x; wb[4 * c + 1] = v.y; wb[4 * c + 2] = v.z; wb[4 * c + 3] = v.w;
-              read_words |= v.x;                 // a word of every load
-            }
-#pragma unroll
-            for (int g = 0; g < kHalfTok / 4; ++g) {
-              float f[4];
-              unpack_f24(wb + 3 * g, f);
-#pragma unroll
-              for (int k = 0; k < 4; ++k) s[4 * g + k] = rcv ? s[4 * g + k] + f[k] : 0.0f;
-            }
-          }
-          __syncwarp();
-          // The received words are in registers: release the buffer to the partner without a
-          // release fence (which would wait for this warp's remote stores), and re-arm it for
-          // tile jj + 2 (the partner sends that only after all four owner warps released it).
-          if (lane == 1)
-            mbar_arrive_remote_relaxed(
-                released_by(sb ? xs_free_r1 : xs_free_r0, read_words, p.zero));
-          if (sp == 0 && lane == 0 && rcv) mbar_arrive_expect_tx_relaxed(&xs_full[sb], kXsBytes);
-
-          // ---- online softmax of row n over this tile (log2 domain, lazy reference) ----
-          if (pos0 + kHalfTok - 1 > lim) {
-#pragma unroll
-            for (int c = 0; c < kHalfTok; ++c)
-              if (pos0 + c > lim) s[c] = -INFINITY;
-          }
-          float mt[kHalfTok / 2];
-#pragma unroll
-          for (int c = 0; c < kHalfTok / 2; ++c) mt[c] = fmaxf(s[c], s[c + kHalfTok / 2]);
-#pragma unroll
-          for (int w2 = kHalfTok / 4; w2 >= 1; w2 >>= 1)
-#pragma unroll
-            for (int c = 0; c < w2; ++c) mt[c] = fmaxf(mt[c], mt[c + w2]);
-          const float mh = mt[0] * c_log2;
-          const float mx = fmaxf(mh, __shfl_xor_sync(0xffffffffu, mh, 16));
-          float alpha = 1.0f;
-          if (mx > mref + kLazyThreshold) {
-            alpha = ex2_approx(mref - mx);       // 0 while mref is still kRefInit
-            l *= alpha;
-            mref = mx;
-          }
-          // O rows of an earlier tile of the piece: rescale (the first tile overwrites O)
-          if (t > tb && __any_sync(0xffffffffu, alpha != 1.0f)) rescale_o(jj, alpha);
-          // weights 2^(s * scale - m) over the S buffer (its scores are in registers)
-          uint32_t pk[kHalfTok / 2];
-          float sa = 0.0f, sc = 0.0f;
-#pragma unroll
-          for (int c = 0; c < kHalfTok / 2; ++c) {
-            const float p0 = ex2_approx(fmaf(s[2 * c], c_log2, -mref));
-            const float p1 = ex2_approx(fmaf(s[2 * c + 1], c_log2, -mref));
-            sa += p0;
-            sc += p1;
-            pk[c] = cvt_bf16x2(p0, p1);
-          }
-          l += sa + sc;
-          lt = l + __shfl_xor_sync(0xffffffffu, l, 16);
-          if (jj >= 2) {
-            __all_sync(0xffffffffu, mbar_wait(&pv_done[sb], ((jj - 2) >> 1) & 1, wc));
+      if constexpr (role == 0) {
+        // ------------- owner: this CTA's 16 rows of sub-partition sp; softmax and P ---------
+        const int qi = row / p.num_heads;
+        load_q(sched[0]);
+        UnitWalk w{sched[0], sched[1]};
+        w.load(p, cg);
+        int jj = 0;
+        SlotRing ring(p.nslot);
+        while (true) {
+          const int tb = max(w.s, r0), te = min(w.s + w.tiles, r1);
+          const int L = w.L;
+          // last position row n sees (causal: L - q + i); rows past q*H see L - 1
+          const int lim = min(L - 1, p.causal ? L - p.q_len + qi : L - 1);
+          float mref = kRefInit, l = 0.0f, lt = 0.0f;   // the same in both threads of a row
+          for (int t = tb; t < te; ++t, ++jj, ring.next()) {
+            const int sb = jj & 1;                 // S buffer and partial buffer of this tile
+            const int slot = ring.slot;
+            const int tile_pos0 = (t - w.s) * kDecodeTok;
+            const int pos0 = tile_pos0 + qt * kHalfTok;   // first token of this thread's half
+            // ---- own partial scores ----
+            float s[kHalfTok];
+            const bool got = __all_sync(0xffffffffu, mbar_wait(&s_full[sb], (jj >> 1) & 1, wc));
             tc_fence_after();
-          }
-          tm_st_x16_s16(trow + kColP + 32 * sb, pk);
-          // ---- the same weights, the rescale factor and the running sum to the partner ----
-          const bool pfree =
-              __all_sync(0xffffffffu, jj == 0 || mbar_wait_cluster(xp_free, (jj - 1) & 1, wc));
-          if (pfree) {
+            if (got) {
+              tm_ld_x32_s32(trow + kColS + 64 * sb, s);
+              tmem_wait_ld();
+            } else {
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              st_async_v4(xp_r + xp_offset(m, 4 * qt + k),
-                          make_uint4(pk[4 * k], pk[4 * k + 1], pk[4 * k + 2], pk[4 * k + 3]),
-                          xp_full_r);
-            if (qt == 0)
-              st_async_v2(xp_r + xp_scalars(m),
-                          make_uint2(__float_as_uint(alpha), __float_as_uint(lt)), xp_full_r);
-          }
-          if (tr) MLA_PTRACE(6, jj);
-          // cache rows past the context may hold anything (even NaN): zero their latent half
-          // so that 0-weight x garbage cannot reach O
-          if (!Q8 && tile_pos0 + kDecodeTok > L) {
-            const int tid = sp * 32 + lane;      // 0..127
-            const int tok = tid & (kDecodeTok - 1);
-            if (tile_pos0 + tok >= L) {
-              uint8_t* sbase = slots + slot * lay.slot_bytes;
-              for (int k = tid >> 6; k < lb; k += 2) {
-                uint4* rowp = reinterpret_cast<uint4*>(sbase + k * kBlk + tok * 128);
+              for (int c = 0; c < kHalfTok; ++c) s[c] = 0.0f;
+            }
+            if (tr) MLA_PTRACE(10, jj);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s_free[sb]);
+            // S of the piece's last tile is complete: the next piece's Q may replace this one
+            if (t == te - 1 && w.s + w.tiles < r1) load_q(w.b + 1);
+            // ---- plus the partner's partial ----
+            const bool rcv =
+                __all_sync(0xffffffffu, mbar_wait_cluster(&xs_full[sb], (jj >> 1) & 1, wc));
+            if (tr) MLA_PTRACE(5, jj);
+            uint32_t read_words = 0;
+            {
+              const uint32_t src = xs_s + sb * kXsBytes;
+              uint32_t wb[kPackWords];
 #pragma unroll
-                for (int ch = 0; ch < 8; ++ch) rowp[ch] = make_uint4(0, 0, 0, 0);
+              for (int c = 0; c < kPackWords / 4; ++c) {
+                const uint4 v = ld_shared_v4(src + xs_offset(sp, lane, c));
+                wb[4 * c] = v.x; wb[4 * c + 1] = v.y; wb[4 * c + 2] = v.z; wb[4 * c + 3] = v.w;
+                read_words |= v.x;                 // a word of every load
+              }
+#pragma unroll
+              for (int g = 0; g < kHalfTok / 4; ++g) {
+                float f[4];
+                unpack_f24(wb + 3 * g, f);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) s[4 * g + k] = rcv ? s[4 * g + k] + f[k] : 0.0f;
               }
             }
-          }
-          // P (and any O rescale and zeroed rows) complete: hand the tile to the PV issuer
-          tmem_wait_st();
-          fence_proxy_async_smem();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&p_full[sb]);
-        }
-        // ---- epilogue of this piece: O and lse of the own rows ----
-        bool aborted = false;
-        write_o(w, tb, te, jj - 1, lt, &aborted);
-        if (row_ok && qt == 0) {
-          const float lse = (lt > 0.0f && !aborted) ? (mref + __log2f(lt)) * kLn2 : -INFINITY;
-          const bool whole = (tb == w.s) && (te == w.s + w.tiles);
-          if (whole) p.lse[int64_t(w.b) * p.qH + row] = lse;
-          else p.part_lse[int64_t(piece_slot(vc, w.s, per, p.col_groups, cg)) * kPairRows + n] = lse;
-        }
-        w.s += w.tiles;
-        ++w.b;
-        if (w.s >= r1) break;
-        w.load(p, cg);
-      }
-    } else if constexpr (role == 1) {
-      // ------------- sender: the partner's 16 rows of sub-partition sp, partial scores ----
-      load_q(sched[0]);
-      UnitWalk w{sched[0], sched[1]};
-      int jj = 0;
-      for (; w.s < r1; w.s += w.tiles, ++w.b) {
-        w.load(p, cg);
-        const int tb = max(w.s, r0), te = min(w.s + w.tiles, r1);
-        for (int t = tb; t < te; ++t, ++jj) {
-          const int sb = jj & 1;
-          float x[kHalfTok];
-          const bool got = __all_sync(0xffffffffu, mbar_wait(&s_full[sb], (jj >> 1) & 1, wc));
-          tc_fence_after();
-          if (got) {
-            tm_ld_x32_s32(trow + kColS + 64 * sb, x);
-            tmem_wait_ld();
-          } else {
+            __syncwarp();
+            // The received words are in registers: release the buffer to the partner without a
+            // release fence (which would wait for this warp's remote stores), and re-arm it for
+            // tile jj + 2 (the partner sends that only after all four owner warps released it).
+            if (lane == 1)
+              mbar_arrive_remote_relaxed(
+                  released_by(sb ? xs_free_r1 : xs_free_r0, read_words, p.zero));
+            if (sp == 0 && lane == 0 && rcv) mbar_arrive_expect_tx_relaxed(&xs_full[sb], kXsBytes);
+
+            // ---- online softmax of row n over this tile (log2 domain, lazy reference) ----
+            if (pos0 + kHalfTok - 1 > lim) {
 #pragma unroll
-            for (int c = 0; c < kHalfTok; ++c) x[c] = 0.0f;
-          }
-          if (tr) MLA_PTRACE(3, jj);
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&s_free[sb]);
-          if (t == te - 1 && w.s + w.tiles < r1) load_q(w.b + 1);
-          uint32_t pw[kPackWords];
-#pragma unroll
-          for (int g = 0; g < kHalfTok / 4; ++g) pack_f24(x + 4 * g, pw + 3 * g);
-          // into the partner's buffer sb once its owners consumed tile jj - 2 from it: stores
-          // from registers over the SM-to-SM network, completing on the partner's mbarrier.
-          // The partner's owner thread of this (row, half) is the same lane of its warp sp.
-          const bool free_ok = __all_sync(
-              0xffffffffu, jj < 2 || mbar_wait_cluster(&xs_free[sb], ((jj - 2) >> 1) & 1, wc));
-          if (free_ok) {
-            const uint32_t dst = xs_r + sb * kXsBytes;
-            const uint32_t rb = sb ? xs_full_r1 : xs_full_r0;
-#pragma unroll
-            for (int c = 0; c < kPackWords / 4; ++c)
-              st_async_v4(dst + xs_offset(sp, lane, c),
-                          make_uint4(pw[4 * c], pw[4 * c + 1], pw[4 * c + 2], pw[4 * c + 3]), rb);
-          }
-          if (tr) MLA_PTRACE(4, jj);
-        }
-      }
-    } else {
-      // ------------- receiver: the partner's weights for its 16 rows of sub-partition sp --
-      UnitWalk w{sched[0], sched[1]};
-      w.load(p, cg);
-      int jj = 0;
-      while (true) {
-        const int tb = max(w.s, r0), te = min(w.s + w.tiles, r1);
-        float lt = 0.0f;
-        for (int t = tb; t < te; ++t, ++jj) {
-          const int sb = jj & 1;
-          const bool rcv = __all_sync(0xffffffffu, mbar_wait_cluster(xp_full, jj & 1, wc));
-          if (tr) MLA_PTRACE(7, jj);
-          uint32_t pk[kHalfTok / 2];
-          uint32_t read_words = 0;               // a word of every load
-          float alpha = 1.0f;
-          if (rcv) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const uint4 v = ld_shared_v4(xp_s + xp_offset(m, 4 * qt + k));
-              pk[4 * k] = v.x; pk[4 * k + 1] = v.y; pk[4 * k + 2] = v.z; pk[4 * k + 3] = v.w;
-              read_words |= v.x;
+              for (int c = 0; c < kHalfTok; ++c)
+                if (pos0 + c > lim) s[c] = -INFINITY;
             }
-            const uint2 sv = ld_shared_v2(xp_s + xp_scalars(m));
-            read_words |= sv.x;
-            alpha = __uint_as_float(sv.x);
-            lt = __uint_as_float(sv.y);
-          } else {
+            float mt[kHalfTok / 2];
 #pragma unroll
-            for (int c = 0; c < kHalfTok / 2; ++c) pk[c] = 0u;
-            lt = 0.0f;
+            for (int c = 0; c < kHalfTok / 2; ++c) mt[c] = fmaxf(s[c], s[c + kHalfTok / 2]);
+#pragma unroll
+            for (int w2 = kHalfTok / 4; w2 >= 1; w2 >>= 1)
+#pragma unroll
+              for (int c = 0; c < w2; ++c) mt[c] = fmaxf(mt[c], mt[c + w2]);
+            const float mh = mt[0] * c_log2;
+            const float mx = fmaxf(mh, __shfl_xor_sync(0xffffffffu, mh, 16));
+            float alpha = 1.0f;
+            if (mx > mref + kLazyThreshold) {
+              alpha = ex2_approx(mref - mx);       // 0 while mref is still kRefInit
+              l *= alpha;
+              mref = mx;
+            }
+            // O rows of an earlier tile of the piece: rescale (the first tile overwrites O)
+            if (t > tb && __any_sync(0xffffffffu, alpha != 1.0f)) rescale_o(jj, alpha);
+            // weights 2^(s * scale - m) over the S buffer (its scores are in registers)
+            uint32_t pk[kHalfTok / 2];
+            float sa = 0.0f, sc = 0.0f;
+#pragma unroll
+            for (int c = 0; c < kHalfTok / 2; ++c) {
+              const float p0 = ex2_approx(fmaf(s[2 * c], c_log2, -mref));
+              const float p1 = ex2_approx(fmaf(s[2 * c + 1], c_log2, -mref));
+              sa += p0;
+              sc += p1;
+              pk[c] = cvt_bf16x2(p0, p1);
+            }
+            l += sa + sc;
+            lt = l + __shfl_xor_sync(0xffffffffu, l, 16);
+            if (jj >= 2) {
+              __all_sync(0xffffffffu, mbar_wait(&pv_done[sb], ((jj - 2) >> 1) & 1, wc));
+              tc_fence_after();
+            }
+            tm_st_x16_s16(trow + kColP + 32 * sb, pk);
+            // ---- the same weights, the rescale factor and the running sum to the partner ----
+            const bool pfree =
+                __all_sync(0xffffffffu, jj == 0 || mbar_wait_cluster(xp_free, (jj - 1) & 1, wc));
+            if (pfree) {
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                st_async_v4(xp_r + xp_offset(m, 4 * qt + k),
+                            make_uint4(pk[4 * k], pk[4 * k + 1], pk[4 * k + 2], pk[4 * k + 3]),
+                            xp_full_r);
+              if (qt == 0)
+                st_async_v2(xp_r + xp_scalars(m),
+                            make_uint2(__float_as_uint(alpha), __float_as_uint(lt)), xp_full_r);
+            }
+            if (tr) MLA_PTRACE(6, jj);
+            // cache rows past the context may hold anything (even NaN): zero their latent half
+            // so that 0-weight x garbage cannot reach O
+            if (!Q8 && tile_pos0 + kDecodeTok > L) {
+              const int tid = sp * 32 + lane;      // 0..127
+              const int tok = tid & (kDecodeTok - 1);
+              if (tile_pos0 + tok >= L) {
+                uint8_t* sbase = slots + slot * lay.slot_bytes;
+                for (int k = tid >> 6; k < lb; k += 2) {
+                  uint4* rowp = reinterpret_cast<uint4*>(sbase + k * kBlk + tok * 128);
+#pragma unroll
+                  for (int ch = 0; ch < 8; ++ch) rowp[ch] = make_uint4(0, 0, 0, 0);
+                }
+              }
+            }
+            // P (and any O rescale and zeroed rows) complete: hand the tile to the PV issuer
+            tmem_wait_st();
+            fence_proxy_async_smem();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&p_full[sb]);
           }
-          __syncwarp();
-          // consumed into registers: release the buffer (relaxed) and re-arm it for tile jj + 1
-          if (lane == 1) mbar_arrive_remote_relaxed(released_by(xp_free_r, read_words, p.zero));
-          if (sp == 0 && lane == 0 && rcv) mbar_arrive_expect_tx_relaxed(xp_full, kXpBytes);
-          // the owner moved its reference: rescale these rows of this CTA's O half the same way
-          if (t > tb && __any_sync(0xffffffffu, alpha != 1.0f)) rescale_o(jj, alpha);
-          if (jj >= 2) {
-            __all_sync(0xffffffffu, mbar_wait(&pv_done[sb], ((jj - 2) >> 1) & 1, wc));
-            tc_fence_after();
+          // ---- epilogue of this piece: O and lse of the own rows ----
+          bool aborted = false;
+          write_o(w, tb, te, jj - 1, lt, &aborted);
+          if (row_ok && qt == 0) {
+            const float lse = (lt > 0.0f && !aborted) ? (mref + __log2f(lt)) * kLn2 : -INFINITY;
+            const bool whole = (tb == w.s) && (te == w.s + w.tiles);
+            if (whole) p.lse[int64_t(w.b) * p.qH + row] = lse;
+            else
+              p.part_lse[int64_t(piece_slot(vc, w.s, per, p.col_groups, cg)) * kPairRows + n] = lse;
           }
-          tm_st_x16_s16(trow + kColP + 32 * sb, pk);
-          tmem_wait_st();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&p_full[sb]);
-          if (tr) MLA_PTRACE(11, jj);
+          w.s += w.tiles;
+          ++w.b;
+          if (w.s >= r1) break;
+          w.load(p, cg);
         }
-        // ---- epilogue of this piece: O of the partner's rows (this CTA's latent half) ----
-        bool aborted = false;
-        write_o(w, tb, te, jj - 1, lt, &aborted);
-        w.s += w.tiles;
-        ++w.b;
-        if (w.s >= r1) break;
+      } else if constexpr (role == 1) {
+        // ------------- sender: the partner's 16 rows of sub-partition sp, partial scores ----
+        load_q(sched[0]);
+        UnitWalk w{sched[0], sched[1]};
+        int jj = 0;
+        for (; w.s < r1; w.s += w.tiles, ++w.b) {
+          w.load(p, cg);
+          const int tb = max(w.s, r0), te = min(w.s + w.tiles, r1);
+          for (int t = tb; t < te; ++t, ++jj) {
+            const int sb = jj & 1;
+            float x[kHalfTok];
+            const bool got = __all_sync(0xffffffffu, mbar_wait(&s_full[sb], (jj >> 1) & 1, wc));
+            tc_fence_after();
+            if (got) {
+              tm_ld_x32_s32(trow + kColS + 64 * sb, x);
+              tmem_wait_ld();
+            } else {
+#pragma unroll
+              for (int c = 0; c < kHalfTok; ++c) x[c] = 0.0f;
+            }
+            if (tr) MLA_PTRACE(3, jj);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s_free[sb]);
+            if (t == te - 1 && w.s + w.tiles < r1) load_q(w.b + 1);
+            uint32_t pw[kPackWords];
+#pragma unroll
+            for (int g = 0; g < kHalfTok / 4; ++g) pack_f24(x + 4 * g, pw + 3 * g);
+            // into the partner's buffer sb once its owners consumed tile jj - 2 from it: stores
+            // from registers over the SM-to-SM network, completing on the partner's mbarrier.
+            // The partner's owner thread of this (row, half) is the same lane of its warp sp.
+            const bool free_ok = __all_sync(
+                0xffffffffu, jj < 2 || mbar_wait_cluster(&xs_free[sb], ((jj - 2) >> 1) & 1, wc));
+            if (free_ok) {
+              const uint32_t dst = xs_r + sb * kXsBytes;
+              const uint32_t rb = sb ? xs_full_r1 : xs_full_r0;
+#pragma unroll
+              for (int c = 0; c < kPackWords / 4; ++c)
+                st_async_v4(dst + xs_offset(sp, lane, c),
+                            make_uint4(pw[4 * c], pw[4 * c + 1], pw[4 * c + 2], pw[4 * c + 3]), rb);
+            }
+            if (tr) MLA_PTRACE(4, jj);
+          }
+        }
+      } else {
+        // ------------- receiver: the partner's weights for its 16 rows of sub-partition sp --
+        UnitWalk w{sched[0], sched[1]};
         w.load(p, cg);
+        int jj = 0;
+        while (true) {
+          const int tb = max(w.s, r0), te = min(w.s + w.tiles, r1);
+          float lt = 0.0f;
+          for (int t = tb; t < te; ++t, ++jj) {
+            const int sb = jj & 1;
+            const bool rcv = __all_sync(0xffffffffu, mbar_wait_cluster(xp_full, jj & 1, wc));
+            if (tr) MLA_PTRACE(7, jj);
+            uint32_t pk[kHalfTok / 2];
+            uint32_t read_words = 0;               // a word of every load
+            float alpha = 1.0f;
+            if (rcv) {
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const uint4 v = ld_shared_v4(xp_s + xp_offset(m, 4 * qt + k));
+                pk[4 * k] = v.x; pk[4 * k + 1] = v.y; pk[4 * k + 2] = v.z; pk[4 * k + 3] = v.w;
+                read_words |= v.x;
+              }
+              const uint2 sv = ld_shared_v2(xp_s + xp_scalars(m));
+              read_words |= sv.x;
+              alpha = __uint_as_float(sv.x);
+              lt = __uint_as_float(sv.y);
+            } else {
+#pragma unroll
+              for (int c = 0; c < kHalfTok / 2; ++c) pk[c] = 0u;
+              lt = 0.0f;
+            }
+            __syncwarp();
+            // consumed into registers: release the buffer (relaxed) and re-arm it for tile jj + 1
+            if (lane == 1) mbar_arrive_remote_relaxed(released_by(xp_free_r, read_words, p.zero));
+            if (sp == 0 && lane == 0 && rcv) mbar_arrive_expect_tx_relaxed(xp_full, kXpBytes);
+            // the owner moved its reference: rescale these rows of this CTA's O half the same way
+            if (t > tb && __any_sync(0xffffffffu, alpha != 1.0f)) rescale_o(jj, alpha);
+            if (jj >= 2) {
+              __all_sync(0xffffffffu, mbar_wait(&pv_done[sb], ((jj - 2) >> 1) & 1, wc));
+              tc_fence_after();
+            }
+            tm_st_x16_s16(trow + kColP + 32 * sb, pk);
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&p_full[sb]);
+            if (tr) MLA_PTRACE(11, jj);
+          }
+          // ---- epilogue of this piece: O of the partner's rows (this CTA's latent half) ----
+          bool aborted = false;
+          write_o(w, tb, te, jj - 1, lt, &aborted);
+          w.s += w.tiles;
+          ++w.b;
+          if (w.s >= r1) break;
+          w.load(p, cg);
+        }
       }
-    }
     };
     const int role = (warp - kRowWarp0<Q8>) >> 2;
     if (role == 0) {

@@ -3,8 +3,16 @@
 //
 // A page's codes go from memory to the registers of the dequantising warps and from there, as
 // bf16, into the cache slot: no shared memory holds them in between, which the largest shapes
-// do not have. A warp converts 8 tokens (lane: token lane / 4, 16 of the 64 columns); its loads of the next page are issued as soon as this page's codes have
-// left the registers, and the TMA producer brings pages into L2 ahead of them.
+// do not have. A warp converts 8 tokens (lane: token lane / 4, 16 of the 64 columns); its loads
+// of the next page are issued as soon as this page's codes have left the registers, and the TMA
+// producer brings pages into L2 ahead of them.
+//
+// What this costs is issue slots, which the softmax warps of the same SM need: some 12 cycles of
+// a scheduler for 4 codes of a warp. Against the bf16 cache the 16- and 32-row kernels keep their
+// time (1M tokens 129 us, 128 ragged sequences 433 us: half the bytes for the same time), the
+// 64-row kernel takes 1.3 times (202 us, 156), the two-CTA kernel 1.4 times (266 us, 189).
+// Measured and slower: 16 warps of half the blocks, two pages ahead in registers, converting
+// before the slot is free, S^T begun on half a page.
 #pragma once
 
 #include "decode_sched.cuh"
@@ -48,7 +56,8 @@ struct PageWalk {
 };
 
 // Bring the pages of the tiles up to `upto` (exclusive of r1) into L2; one thread.
-MLA_DEVICE void prefetch_pages(const DecodeParams& p, int cg, int r1, int upto, PageWalk& ahead) {
+MLA_DEVICE void prefetch_pages(const DecodeParams& p, int cg, int r1, int upto,
+                               PageWalk& ahead) {
   const int64_t page_bytes = q8_page_bytes(p.r, p.D - p.r);
   while (ahead.t < r1 && ahead.t <= upto) {
     const int32_t page = ahead.page(p);
@@ -61,7 +70,8 @@ MLA_DEVICE void prefetch_pages(const DecodeParams& p, int cg, int r1, int upto, 
 
 // All pages of tiles [r0, r1), whose first is of sequence b, which starts at tile s. This warp
 // converts the NG 8-token groups from NG * grp on of the page's column blocks [blk0, blk0 + nb),
-// nb <= NB, into the slot's blocks 0, 1, ... It waits for empty[slot] and arrives once on full[slot].
+// nb <= NB, into the slot's blocks 0, 1, ... It waits for empty[slot] and arrives on full[slot]
+// once.
 template <int NB, int NG>
 MLA_DEVICE void dequant_pages(const DecodeParams& p, int cg, int r0, int r1, int b, int s, int grp,
                               int blk0, int nb, uint8_t* slots, uint32_t slot_bytes,
@@ -89,7 +99,8 @@ MLA_DEVICE void dequant_pages(const DecodeParams& p, int cg, int r0, int r1, int
     for (int g = 0; g < NG; ++g) {
 #pragma unroll
       for (int k = 0; k < NB; ++k)
-        if (k < nb) codes[g][k] = ld_stream_v4(src + code_off + k * kQ8BlockBytes + g * 8 * kQ8Cols);
+        if (k < nb)
+          codes[g][k] = ld_stream_v4(src + code_off + k * kQ8BlockBytes + g * 8 * kQ8Cols);
       scales[g] = *reinterpret_cast<const uint2*>(src + scale_off + g * 8 * kQ8ScaleBytes);
     }
     next.next(p, cg, r1);

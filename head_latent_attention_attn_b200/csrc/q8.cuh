@@ -23,7 +23,7 @@ constexpr int kQ8Cols = 64;            // latent columns per scale
 constexpr int kQ8MaxBlocks = 8;        // r <= 512
 constexpr int kQ8BlockBytes = kQ8Tok * kQ8Cols;
 constexpr int kQ8ScaleBytes = kQ8MaxBlocks;   // per token
-constexpr int kQ8ExpMin = -110;        // smallest scale 2^-110: every nonzero value is a normal bf16
+constexpr int kQ8ExpMin = -110;        // 2^-110: every nonzero value is a normal bf16
 constexpr int kQ8ExpMax = 119;         // largest scale 2^119: 448 * 2^119 is finite in bf16
 constexpr uint32_t kQ8Bad = 255;       // scale byte of a block with a non-finite value
 
