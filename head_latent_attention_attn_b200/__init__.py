@@ -156,13 +156,12 @@ _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
-def _call(fn, what: str, stream, dims: MlaDims, *args) -> None:
-    """fn(dims, *args, stream) on the device that holds all tensors among `args` (passed as
-    their addresses), on `stream` or that device's current stream; raises on a status."""
-    tensors = [x for x in args if x.__class__ is not int and isinstance(x, torch.Tensor)]
+def _call(fn, what: str, stream, dims: MlaDims, tensors, *args) -> None:
+    """fn(dims, *args, stream) on the device that holds all of `tensors` (None entries aside), on
+    `stream` or that device's current stream; raises on a status."""
     dev = tensors[0].get_device()
     for t in tensors:
-        if t.get_device() != dev:
+        if t is not None and t.get_device() != dev:
             raise MlaError(f"{what}: tensors are on cuda:{dev} and {t.device}",
                            MLA_ERR_INVALID_ARG)
     if stream is None:
@@ -174,14 +173,17 @@ def _call(fn, what: str, stream, dims: MlaDims, *args) -> None:
         stream = stream.cuda_stream
     else:
         stream = int(stream)
-    a = [x if x is None or x.__class__ is int else x.data_ptr() for x in args]
     if dev == torch.cuda.current_device():
-        st = fn(ctypes.byref(dims), *a, stream)
+        st = fn(ctypes.byref(dims), *args, stream)
     else:
         with torch.cuda.device(dev):
-            st = fn(ctypes.byref(dims), *a, stream)
+            st = fn(ctypes.byref(dims), *args, stream)
     if st != MLA_OK:
         _check(st, what)
+
+
+def _addr(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
 
 
 def _check(status: int, what: str) -> None:
@@ -190,6 +192,9 @@ def _check(status: int, what: str) -> None:
 
 
 def _need(t, name: str, dtype, shape=None, cuda: bool = True) -> None:
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.is_cuda and t.is_contiguous() and
+            (shape is None or t.shape == shape)):    # torch.Size is a tuple
+        return
     if not isinstance(t, torch.Tensor):
         raise MlaError(f"{name} must be a torch.Tensor", MLA_ERR_INVALID_ARG)
     if cuda and not t.is_cuda:
@@ -198,7 +203,7 @@ def _need(t, name: str, dtype, shape=None, cuda: bool = True) -> None:
         raise MlaError(f"{name} must be {dtype}, got {t.dtype}", MLA_ERR_INVALID_ARG)
     if not t.is_contiguous():
         raise MlaError(f"{name} must be contiguous", MLA_ERR_INVALID_ARG)
-    if shape is not None and t.shape != shape:     # torch.Size is a tuple
+    if shape is not None and tuple(t.shape) != tuple(shape):
         raise MlaError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}",
                        MLA_ERR_INVALID_ARG)
 
@@ -396,9 +401,10 @@ def mla_cache_append_q8(dims: MlaDims, c_kv, k_r, rope_cos, rope_sin, block_tabl
     G, dr, r = dims.num_kv_groups, dims.rope_dim, dims.kv_lora_rank
     _need(c_kv, "c_kv", torch.bfloat16, (B, n, r))
     if dr > 0:
+        angles = (B, n, G, dr // 2)
         _need(k_r, "k_r", torch.bfloat16, (B, n, G, dr))
-        _need(rope_cos, "rope_cos", torch.float32, (B, n, G, dr // 2))
-        _need(rope_sin, "rope_sin", torch.float32, (B, n, G, dr // 2))
+        _need(rope_cos, "rope_cos", torch.float32, angles)
+        _need(rope_sin, "rope_sin", torch.float32, angles)
     else:
         k_r = rope_cos = rope_sin = None
     _need_q8(dims, cache, block_table, B)
@@ -407,9 +413,11 @@ def mla_cache_append_q8(dims: MlaDims, c_kv, k_r, rope_cos, rope_sin, block_tabl
         _need(new_lens, "new_lens", torch.int32, (B,))
     if dev_error is not None:
         _need(dev_error, "dev_error", torch.int32)
-    _call(lib().mla_cache_append_q8, "mla_cache_append_q8", stream, dims, c_kv, k_r, rope_cos,
-          rope_sin, block_table, block_table.shape[1], start_pos, new_lens, B, n, cache,
-          cache.shape[0], dev_error)
+    _call(lib().mla_cache_append_q8, "mla_cache_append_q8", stream, dims,
+          (c_kv, k_r, rope_cos, rope_sin, block_table, start_pos, new_lens, cache, dev_error),
+          c_kv.data_ptr(), _addr(k_r), _addr(rope_cos), _addr(rope_sin), block_table.data_ptr(),
+          block_table.shape[1], start_pos.data_ptr(), _addr(new_lens), B, n, cache.data_ptr(),
+          cache.shape[0], _addr(dev_error))
 
 
 def mla_cache_read_q8(dims: MlaDims, cache, block_table, start_pos, out, read_lens=None,
@@ -426,8 +434,10 @@ def mla_cache_read_q8(dims: MlaDims, cache, block_table, start_pos, out, read_le
         _need(read_lens, "read_lens", torch.int32, (B,))
     if dev_error is not None:
         _need(dev_error, "dev_error", torch.int32)
-    _call(lib().mla_cache_read_q8, "mla_cache_read_q8", stream, dims, cache, cache.shape[0],
-          block_table, block_table.shape[1], start_pos, read_lens, B, n, out, dev_error)
+    _call(lib().mla_cache_read_q8, "mla_cache_read_q8", stream, dims,
+          (cache, block_table, start_pos, read_lens, out, dev_error), cache.data_ptr(),
+          cache.shape[0], block_table.data_ptr(), block_table.shape[1], start_pos.data_ptr(),
+          _addr(read_lens), B, n, out.data_ptr(), _addr(dev_error))
 
 
 def mla_decode_q8_workspace_size(dims: MlaDims, batch: int, q_len: int, max_seq_len: int,
@@ -453,18 +463,20 @@ def mla_decode_attn_q8(dims: MlaDims, q_ext, cache, block_table, seq_lens, max_s
     _need(o_latent, "o_latent", torch.bfloat16, (B, q, H, r))
     _need(lse, "lse", torch.float32, (B, q, H))
     _need(workspace, "workspace", torch.uint8)
-    _call(lib().mla_decode_attn_q8, "mla_decode_attn_q8", stream, dims, q_ext, cache,
-          cache.shape[0], block_table, block_table.shape[1], seq_lens, B, q, int(max_seq_len),
-          1 if causal else 0, int(num_splits), workspace, workspace.numel(), o_latent, lse)
+    _call(lib().mla_decode_attn_q8, "mla_decode_attn_q8", stream, dims,
+          (q_ext, cache, block_table, seq_lens, workspace, o_latent, lse), q_ext.data_ptr(),
+          cache.data_ptr(), cache.shape[0], block_table.data_ptr(), block_table.shape[1],
+          seq_lens.data_ptr(), B, q, int(max_seq_len), 1 if causal else 0, int(num_splits),
+          workspace.data_ptr(), workspace.numel(), o_latent.data_ptr(), lse.data_ptr())
 
 
 def _per_token(t, name: str, shape):
     """Token and head strides of a bf16 CUDA tensor [B, n, heads, width] whose last dim is
     contiguous and whose batches follow one another. (The stride of a dim of size 1 says
     nothing.)"""
-    if not isinstance(t, torch.Tensor) or t.device.type != "cuda" or t.dtype != torch.bfloat16:
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype is not torch.bfloat16:
         raise MlaError(f"{name} must be a bfloat16 CUDA tensor", MLA_ERR_INVALID_ARG)
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise MlaError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}",
                        MLA_ERR_INVALID_ARG)
     B, n, heads, width = shape
@@ -510,9 +522,11 @@ def mla_prefill_attn(dims: MlaDims, q, k_nope, k_pe, v, seq_lens, o, lse, q_lens
         _need(q_lens, "q_lens", torch.int32, (B,))
     if dev_error is not None:
         _need(dev_error, "dev_error", torch.int32)
-    _call(lib().mla_prefill_attn, "mla_prefill_attn", stream, dims, q, k_nope, k_tok, k_head, k_pe,
-          kr_tok, v, v_tok, v_head, seq_lens, q_lens, B, ql, n, 1 if causal else 0, o, lse,
-          dev_error)
+    _call(lib().mla_prefill_attn, "mla_prefill_attn", stream, dims,
+          (q, k_nope, k_pe, v, seq_lens, q_lens, o, lse, dev_error), q.data_ptr(),
+          k_nope.data_ptr(), k_tok, k_head, _addr(k_pe), kr_tok, v.data_ptr(), v_tok, v_head,
+          seq_lens.data_ptr(), _addr(q_lens), B, ql, n, 1 if causal else 0, o.data_ptr(),
+          lse.data_ptr(), _addr(dev_error))
 
 
 def mla_kv_shared_decode_dims(dims: MlaDims) -> MlaDims:

@@ -123,13 +123,12 @@ MLA_DEVICE void dequant_pages(const DecodeParams& p, int cg, int r0, int r1, int
 #pragma unroll
         for (int k = 0; k < NB; ++k) codes[g][k] = make_uint4(0, 0, 0, 0);
       }
+      const uint64_t sc = (uint64_t(scales[g].y) << 32 | scales[g].x) >> (8 * blk0);
 #pragma unroll
       for (int k = 0; k < NB; ++k) {
         if (k >= nb) break;
-        const uint32_t sc =
-            uint32_t((uint64_t(scales[g].y) << 32 | scales[g].x) >> (8 * (blk0 + k))) & 0xFFu;
         uint32_t v[8];
-        q8_decode16(codes[g][k], q8_factor(sc), v);
+        q8_decode16(codes[g][k], q8_factor(uint32_t(sc >> (8 * k)) & 0xFFu), v);
         st_shared_v4(at + k * kBlk8Bytes + g * 1024, v);
         st_shared_v4((at ^ 16u) + k * kBlk8Bytes + g * 1024, v + 4);
       }
