@@ -100,6 +100,7 @@ struct ReadQ8Params {
   int32_t* dev_error;
   int64_t num_pages;
   int32_t max_pages, batch, n, r, R;
+  int32_t wide;              // rows of `out` start on 32-byte boundaries (set by the launch)
 };
 cudaError_t launch_cache_read_q8(const ReadQ8Params& p, cudaStream_t stream);
 

@@ -191,6 +191,26 @@ def test_read_back_is_exact(name, n, start):
     assert mla.mla_get_device_status(err) == mla.MLA_OK
 
 
+@pytest.mark.parametrize("shift", [0, 8, 16, 24])
+def test_read_back_to_rows_on_any_16_bytes(shift):
+    """Rows that start `shift` bf16 numbers behind a 512-byte boundary: the same bits, and nothing
+    outside them."""
+    f = Filled("hybrid", [130, 64], seed=shift)
+    B, n, D = 2, 130, f.dims.row_width
+    buf = torch.full((B * n * D + 64,), 7.0, dtype=torch.bfloat16, device="cuda")
+    out = buf[shift:shift + B * n * D].view(B, n, D)
+    lens = torch.tensor(f.lens, dtype=torch.int32, device="cuda")
+    mla.mla_cache_read_q8(f.dims, f.cache, cu(f.table), torch.zeros_like(lens), out, read_lens=lens,
+                          dev_error=f.err)
+    want = Q.rows(f.cache.cpu().numpy(), 256, 64)
+    got = Q.bf16_to_f64(bits_of(out))
+    for b in range(B):
+        pos = np.arange(f.lens[b])
+        assert np.array_equal(got[b, :f.lens[b]], want[f.table[b, pos // 64], pos % 64])
+        assert np.all(got[b, f.lens[b]:] == 7.0)
+    assert torch.all(buf[:shift] == 7.0) and torch.all(buf[shift + B * n * D:] == 7.0)
+
+
 def test_faults_are_flagged_and_skipped():
     """Bad page ids, positions past the table or below zero and counts outside [0, n] set the
     bounds bit; what they cover is not written or read, and the rest is."""
