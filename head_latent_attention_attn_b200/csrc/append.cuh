@@ -10,23 +10,24 @@
 
 namespace mla {
 
-// Rotary key of every group of one token, one pair (x_j, x_{j + d_r/2}) per lane and step:
-// fp32 with separately rounded products and sums, then bf16 with ties to even.
+// One rotary pair: fp32 with separately rounded products and sums, then bf16 with ties to even.
+MLA_DEVICE void rotate_pair(uint16_t k0, uint16_t k1, float c, float s, uint16_t* y0, uint16_t* y1) {
+  const float x0 = bf16_bits_to_f32(k0);
+  const float x1 = bf16_bits_to_f32(k1);
+  *y0 = f32_to_bf16_rne(__fsub_rn(__fmul_rn(x0, c), __fmul_rn(x1, s)));
+  *y1 = f32_to_bf16_rne(__fadd_rn(__fmul_rn(x1, c), __fmul_rn(x0, s)));
+}
+
+// Rotary key of every group of one token, by `lanes` lanes, one pair (x_j, x_{j + d_r/2}) per lane
+// and step.
 MLA_DEVICE void rotate_keys(const uint16_t* kr, const float* cs, const float* sn, int groups,
-                            int rope_dim, int lane, uint16_t* dst) {
+                            int rope_dim, int lane, uint16_t* dst, int lanes = 32) {
   const int half = rope_dim / 2;
   const int npairs = groups * half;
-  for (int idx = lane; idx < npairs; idx += 32) {
+  for (int idx = lane; idx < npairs; idx += lanes) {
     const int g = idx / half;
-    const int j = idx - g * half;
-    const float x0 = bf16_bits_to_f32(kr[g * rope_dim + j]);
-    const float x1 = bf16_bits_to_f32(kr[g * rope_dim + j + half]);
-    const float c = cs[idx];
-    const float s = sn[idx];
-    const float y0 = __fsub_rn(__fmul_rn(x0, c), __fmul_rn(x1, s));
-    const float y1 = __fadd_rn(__fmul_rn(x1, c), __fmul_rn(x0, s));
-    dst[g * rope_dim + j] = f32_to_bf16_rne(y0);
-    dst[g * rope_dim + j + half] = f32_to_bf16_rne(y1);
+    const int at = g * half + idx;             // g * rope_dim + j
+    rotate_pair(kr[at], kr[at + half], cs[idx], sn[idx], &dst[at], &dst[at + half]);
   }
 }
 

@@ -86,6 +86,7 @@ struct AppendQ8Params {
   int32_t* dev_error;
   int64_t num_pages;
   int32_t max_pages, batch, n_new, r, groups, rope_dim;
+  int32_t quads;             // four rotary pairs can move at once (set by the launch)
 };
 cudaError_t launch_cache_append_q8(const AppendQ8Params& p, cudaStream_t stream);
 

@@ -161,6 +161,74 @@ def test_append_is_the_definition(name, n):
     assert np.array_equal(a[untouched], before[:, sc].reshape(P, 64, 8)[untouched])
 
 
+@pytest.mark.parametrize("name", ["deepseek_v2", "qwen25_7b", "no_rope", "rank_192", "rank_448", "one_head"])
+@pytest.mark.parametrize("shift", [0, 1])
+def test_append_of_many_tokens(name, shift):
+    """Enough tokens for warps of several: every byte as defined, with counts that end inside a warp,
+    a count out of range and pages that are not there; keys and angles that start on any element."""
+    H, G, r, dr = SHAPES[name]
+    R, B, n, P = G * dr, 5, 1003, 90
+    rng = np.random.default_rng(shift + r)
+    start = rng.integers(0, 70, B).astype(np.int32)
+    lens = np.array([n, 0, 515, n + 1, n], np.int32)        # n + 1: appends none, flagged
+    maxp = (70 + n + 63) // 64
+    table = rng.permutation(P)[:B * maxp].reshape(B, maxp).astype(np.int32)
+    table[0, 3], table[4, 5] = -1, P
+    bits = to_bits(rng.standard_normal((B, n, r)) * np.exp(2 * rng.standard_normal((B, n, 1))))
+    bits[0, :, 63], bits[2, 100, 0] = 0x7F80, 0x7FC1
+    bits[4, 7] = 0x0003                                     # subnormals
+    k_bits = to_bits(rng.standard_normal((B, n, G, dr)) * 3)
+    ang = rng.uniform(-40, 40, (B, n, G, dr // 2))
+    cos, sin = np.cos(ang).astype(np.float32), np.sin(ang).astype(np.float32)
+
+    def at(x):                                              # contiguous, `shift` elements in
+        flat = torch.cat([x.new_zeros(shift), x.flatten()])
+        return flat[shift:].view(x.shape)
+
+    before = rng.integers(0, 256, (P, Q.page_bytes(r, R))).astype(np.uint8)
+    want = Q.append(before, bits, k_bits, cos, sin, table, start, np.where(lens > n, 0, lens))
+    cache, err = cu(before), torch.zeros(1, dtype=torch.int32, device="cuda")
+    mla.mla_cache_append_q8(dims_of(name), bf(bits), at(bf(k_bits)), at(cu(cos)), at(cu(sin)),
+                            cu(table), cu(start), cache, new_lens=cu(lens), dev_error=err)
+    assert mla.mla_get_device_status(err) == mla.MLA_ERR_DEVICE_BOUNDS
+    got = cache.cpu().numpy()
+    sc = slice(Q.PS * (r + 2 * R), None)
+    a, b = got[:, sc].reshape(P, 64, 8), want[:, sc].reshape(P, 64, 8)
+    assert np.array_equal(a[..., :r // 64], b[..., :r // 64])
+    written = np.zeros((P, 64), bool)
+    for s in range(B):
+        pos = start[s] + np.arange(0 if lens[s] > n else lens[s])
+        page = table[s, pos // 64]
+        ok = (page >= 0) & (page < P)
+        written[page[ok], pos[ok] % 64] = True
+    assert np.array_equal(a[~written], before[:, sc].reshape(P, 64, 8)[~written])
+    got[:, sc] = want[:, sc]
+    bad = np.argwhere(got != want)
+    assert bad.size == 0, f"{len(bad)} bytes differ, first {bad[:4].tolist()}"
+
+
+@pytest.mark.parametrize("dr", [2, 4, 12])
+def test_append_of_narrow_groups(dr):
+    """Rotary groups that four pairs at a time do not divide: the keys as defined."""
+    G, r, B, n, P = 4, 64, 2, 2100, 70
+    dims = mla.make_dims(8, G, r, 128, dr, 128, 64, 0.1)
+    rng = np.random.default_rng(dr)
+    table = rng.permutation(P)[:B * 34].reshape(B, 34).astype(np.int32)
+    bits = to_bits(rng.standard_normal((B, n, r)))
+    k_bits = to_bits(rng.standard_normal((B, n, G, dr)) * 3)
+    ang = rng.uniform(-40, 40, (B, n, G, dr // 2))
+    cos, sin = np.cos(ang).astype(np.float32), np.sin(ang).astype(np.float32)
+    for m in (9, n):
+        before = rng.integers(0, 256, (P, Q.page_bytes(r, G * dr))).astype(np.uint8)
+        zero = np.zeros(B, np.int32)
+        want = Q.append(before, bits[:, :m], k_bits[:, :m], cos[:, :m], sin[:, :m], table, zero)
+        cache = cu(before)
+        mla.mla_cache_append_q8(dims, bf(bits[:, :m]), bf(k_bits[:, :m]), cu(cos[:, :m]), cu(sin[:, :m]),
+                                cu(table), cu(zero), cache)
+        keep = Q.PS * (r + 2 * G * dr)
+        assert np.array_equal(cache.cpu().numpy()[:, :keep], want[:, :keep])
+
+
 @pytest.mark.parametrize("name", ["deepseek_v2", "qwen3_30b_a3b", "no_rope", "rank_192", "one_head"])
 @pytest.mark.parametrize("n,start", [(1, 63), (9, 60), (130, 0), (64, 1)])
 def test_read_back_is_exact(name, n, start):
