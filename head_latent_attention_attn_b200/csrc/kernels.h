@@ -248,6 +248,10 @@ struct PrefillParams {
   int32_t split;             // CTAs (a cluster) that share the tiles of 256 query rows: 1, 2, 4, 8
   float scale_log2;          // softmax_scale * log2(e)
 };
+// Clusters of `split` CTAs of the kernel that are resident at once on the current device (0 on an
+// error), remembered: a cluster's CTAs share a GPC, so that not every SM can be in one.
+constexpr int kPrefillMaxSplit = 8;
+int prefill_max_clusters(int split);
 cudaError_t launch_prefill(const PrefillParams& p, cudaStream_t stream);
 
 // Merge of the per-piece partials of units cut between CTAs (log-sum-exp identity).

@@ -654,8 +654,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float inv = l != 0.0f ? 1.0f / l : 0.0f;        // NaN stays NaN
         const int64_t row = (int64_t(staged.b) * p.q_len + qi) * p.heads + staged.h;
         if (rank == 0) p.lse[row] = l != 0.0f ? (m + __log2f(l)) * kLn2 : -INFINITY;
-        const int cols = 64 * vb / s;            // 8 at least
-        for (int e = rank * cols; e < (rank + 1) * cols && e < p.dv; e += 8) {
+        for (int e = 8 * rank; e < p.dv; e += 8 * s) {
           float o[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
@@ -689,6 +688,40 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   if (warp == 1) tmem_dealloc(tmem, 512);
+}
+
+int prefill_max_clusters(int split) {
+  // by device and cluster size, plus one; 0: not asked yet
+  static std::atomic<int> known[64][kPrefillMaxSplit + 1];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) {
+    cudaGetLastError();
+    return 0;
+  }
+  if (dev < 64) {
+    const int n = known[dev][split].load(std::memory_order_relaxed);
+    if (n > 0) return n - 1;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = unsigned(split);
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.gridDim = dim3(unsigned(split));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmem;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  if (cudaFuncSetAttribute(mla_prefill_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           int(kSmem)) != cudaSuccess ||
+      cudaOccupancyMaxActiveClusters(&n, mla_prefill_kernel<true>, &cfg) != cudaSuccess) {
+    cudaGetLastError();
+    return 0;
+  }
+  if (dev < 64) known[dev][split].store(n + 1, std::memory_order_relaxed);
+  return n;
 }
 
 template <bool kSplit>

@@ -131,6 +131,19 @@ def test_few_and_many_units(name, q, n, lens, q_lens, causal, heads):
         assert torch.equal(o, o2) and torch.equal(lse, lse2)
 
 
+@pytest.mark.parametrize("H", [2, 9, 16, 20, 25, 33, 44, 60, 80])
+@pytest.mark.parametrize("dv", [8, 72, 128])
+def test_clusters_of_every_size(H, dv):
+    """From eight CTAs a unit down to one as the heads grow, and values whose columns they do not
+    share evenly; a sequence too short for each of them to have a tile."""
+    x = make(1, 21, 2100, H, 1, 128, 8, dv, seed=H)
+    d = mla.make_dims(H, 1, 64, 128, 8, dv, 64, 136 ** -0.5)
+    for L, ql in ((2100, 21), (300, 5), (2100, 0)):
+        o, lse, st = run(d, x, [L], [ql])
+        assert st == mla.MLA_OK
+        check(d, x, [L], [ql], True, o, lse, [0, H - 1])
+
+
 def test_rows_that_see_nothing():
     """Contexts of zero, and shorter than the rows (whose first positions are negative)."""
     x = make(4, 200, 150, 4, 1, 128, 64, 128)
