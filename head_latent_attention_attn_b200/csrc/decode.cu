@@ -177,6 +177,39 @@ MLA_DEVICE void tmem_ld_s<32>(uint32_t taddr, float* v) {
       : "memory");
 }
 
+// Column values of 16 lanes joined by `op`, in the steps lane ^ 8, ^ 4, ^ 2, ^ 1; in each but for the
+// last of N = 8, a lane keeps half of its columns and hands over the others, so that all N columns
+// take 2 (N - 2) shuffles less than one at a time. Lane i (of 16) then holds the columns from
+// joined_column<N>(i) on, N / 16 of them, in v[0], ...; with N = 8, two lanes hold each.
+template <int N, class Op>
+MLA_DEVICE void join16(float* v, int lane, Op op) {
+  int n = N;
+#pragma unroll
+  for (int mask = 8; mask > 0; mask >>= 1) {
+    const bool up = (lane & mask) != 0;
+    if (n > 1) {
+      n /= 2;
+#pragma unroll
+      for (int i = 0; i < N / 2; ++i) {
+        if (i >= n) break;
+        const float keep = up ? v[i + n] : v[i], give = up ? v[i] : v[i + n];
+        v[i] = op(keep, __shfl_xor_sync(0xffffffffu, give, mask));
+      }
+    } else {
+      v[0] = op(v[0], __shfl_xor_sync(0xffffffffu, v[0], mask));
+    }
+  }
+}
+MLA_DEVICE float lane4(const float4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
+template <int N>
+MLA_DEVICE int joined_column(int lane) { return N >= 16 ? (lane & 15) * (N / 16) : (lane & 15) / (16 / N); }
+template <int N>
+MLA_DEVICE void store_joined(float* at, const float* v, int lane) {
+  at += joined_column<N>(lane);
+  if (N == 32) *reinterpret_cast<float2*>(at) = make_float2(v[0], v[1]);
+  else *at = v[0];
+}
+
 __host__ __device__ constexpr SmemSwizzle pt_swizzle(int ncol) {
   return ncol == 64 ? kSw128 : (ncol == 32 ? kSw64 : kSw32);
 }
@@ -479,14 +512,14 @@ __global__ void __launch_bounds__(kBlockThreads<Q8>, 1)
             tmem_ld_s<HALF>(s_addr, tt);
             tmem_wait_ld();
           }
+          // row (i, h), column i H + h of the sequence, sees token pos iff pos < L and (causal)
+          // pos <= L - q + i: from this one of the thread's columns on
+          int seen = 0;
           if (ragged) {
-            // row (i, h) sees token pos iff pos < L and (causal) pos <= L - q + i
+            const int need = p.causal ? pos - L + p.q_len : 0;      // least i
+            seen = !got || pos >= L ? HALF : need > 0 ? need * p.num_heads - (cg * NCOL + c0) : 0;
 #pragma unroll
-            for (int j = 0; j < HALF; ++j) {
-              const int qi = (cg * NCOL + c0 + j) / p.num_heads;
-              const bool vis = got && pos < L && (!p.causal || pos <= L - p.q_len + qi);
-              tt[j] = vis ? tt[j] : -INFINITY;
-            }
+            for (int j = 0; j < HALF; ++j) tt[j] = j >= seen ? tt[j] : -INFINITY;
           }
           float tmax = -INFINITY;
 #pragma unroll
@@ -507,33 +540,40 @@ __global__ void __launch_bounds__(kBlockThreads<Q8>, 1)
               tmem_ld_s<HALF>(s_addr, s);
               tmem_wait_ld();
             }
+            {
+              float v[HALF];
 #pragma unroll
-            for (int j = 0; j < HALF; ++j) {
-              if (ragged) {
-                const int qi = (cg * NCOL + c0 + j) / p.num_heads;
-                const bool vis = got && pos < L && (!p.causal || pos <= L - p.q_len + qi);
-                s[j] = vis ? s[j] : -INFINITY;
+              for (int j = 0; j < HALF; ++j) {
+                if (ragged) s[j] = j >= seen ? s[j] : -INFINITY;
+                v[j] = s[j] * c_log2;    // -inf stays -inf
               }
-              float v = s[j] * c_log2;   // -inf stays -inf
-              v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
-              v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
-              v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
-              v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
-              if (col_owner) red[wi * 64 + c0 + j] = v;
+              join16<HALF>(v, lane, [](float a, float b) { return fmaxf(a, b); });
+              store_joined<HALF>(red + wi * 64 + c0, v, lane);
             }
             named_bar_sync(1, 128);
             bool chg = false;
 #pragma unroll
-            for (int j = 0; j < HALF; ++j) {
-              const int n = c0 + j;
-              const float tm = fmaxf(fmaxf(red[n], red[64 + n]), fmaxf(red[128 + n], red[192 + n]));
-              const float mn = fmaxf(m[j], tm);
-              const float a = ex2_approx(m[j] - mn);   // 0 while m is still kRefInit
-              l[j] *= a;
-              m[j] = mn;
-              tt[j] = fmaf(s[j], c_log2, -mn);
-              chg |= a != 1.0f;
-              if (col_owner && wi == 0) alpha_s[n] = a;
+            for (int j0 = 0; j0 < HALF; j0 += 4) {
+              float4 r4[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                r4[i] = *reinterpret_cast<const float4*>(red + 64 * i + c0 + j0);
+              float a4[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int j = j0 + i;
+                const float tm = fmaxf(fmaxf(lane4(r4[0], i), lane4(r4[1], i)),
+                                       fmaxf(lane4(r4[2], i), lane4(r4[3], i)));
+                const float mn = fmaxf(m[j], tm);
+                const float a = ex2_approx(m[j] - mn);   // 0 while m is still kRefInit
+                l[j] *= a;
+                m[j] = mn;
+                tt[j] = fmaf(s[j], c_log2, -mn);
+                chg |= a != 1.0f;
+                a4[i] = a;
+              }
+              if (col_owner && wi == 0)
+                *reinterpret_cast<float4*>(alpha_s + c0 + j0) = make_float4(a4[0], a4[1], a4[2], a4[3]);
             }
             if (col_owner && wi == 0) chg_flag[hf] = chg ? 1 : 0;
             named_bar_sync(1, 128);
@@ -615,23 +655,14 @@ __global__ void __launch_bounds__(kBlockThreads<Q8>, 1)
         const bool fin = __all_sync(0xffffffffu,
                                     mbar_wait(&pv_done[(jj - 1) & 1], ((jj - 1) >> 1) & 1, wc));
         tc_fence_after();
-#pragma unroll
-        for (int j = 0; j < HALF; ++j) {
-          float v = l[j];
-          v += __shfl_xor_sync(0xffffffffu, v, 8);
-          v += __shfl_xor_sync(0xffffffffu, v, 4);
-          v += __shfl_xor_sync(0xffffffffu, v, 2);
-          v += __shfl_xor_sync(0xffffffffu, v, 1);
-          l[j] = v;
-        }
-        named_bar_sync(1, 128);   // every earlier reader of red / mref_s is done
-        if (col_owner) {
-#pragma unroll
-          for (int j = 0; j < HALF; ++j) red[wi * 64 + c0 + j] = l[j];
-        }
+        join16<HALF>(l, lane, [](float a, float b) { return a + b; });
+        named_bar_sync(1, 128);   // every earlier reader of red / mref_s / alpha_s is done
+        store_joined<HALF>(red + wi * 64 + c0, l, lane);
         if (col_owner && wi == 0) {
 #pragma unroll
-          for (int j = 0; j < HALF; ++j) mref_s[c0 + j] = m[j];
+          for (int j = 0; j < HALF; j += 4)
+            *reinterpret_cast<float4*>(mref_s + c0 + j) =
+                make_float4(m[j], m[j + 1], m[j + 2], m[j + 3]);
         }
         named_bar_sync(1, 128);
         const bool aborted = __any_sync(0xffffffffu, !fin || *abort_flag != 0);
@@ -639,23 +670,26 @@ __global__ void __launch_bounds__(kBlockThreads<Q8>, 1)
         const int cols_here = min(NCOL, p.qH - cg * NCOL);
         const int64_t row0 = int64_t(w.b) * p.qH + int64_t(cg) * NCOL;   // first (b, i, h) row
         const int pslot = piece_slot(vc, w.s, per, p.col_groups, cg);
-        if (tid < cols_here) {
+        float* inv_s = alpha_s;   // 1 / sum of every column
+        if (tid < NCOL) {
           const float sum = red[tid] + red[64 + tid] + red[128 + tid] + red[192 + tid];
+          inv_s[tid] = sum > 0.0f ? 1.0f / sum : 0.0f;
           const float lse =
               (sum > 0.0f && !aborted) ? (mref_s[tid] + __log2f(sum)) * kLn2 : -INFINITY;
-          if (whole) p.lse[row0 + tid] = lse;
-          else p.part_lse[int64_t(pslot) * NCOL + tid] = lse;
+          if (tid < cols_here) {
+            if (whole) p.lse[row0 + tid] = lse;
+            else p.part_lse[int64_t(pslot) * NCOL + tid] = lse;
+          }
         }
+        named_bar_sync(1, 128);
+        uint16_t* out = whole ? p.o_latent + row0 * p.r : p.part_o + int64_t(pslot) * NCOL * p.r;
         // O^T: this thread owns latent row 128*c + 32*sp + lane of every chunk c
 #pragma unroll 1
         for (int n0 = 0; n0 < NCOL; n0 += 16) {
           float inv[16];
 #pragma unroll
-          for (int n = 0; n < 16; ++n) {
-            const int col = n0 + n;
-            const float sum = red[col] + red[64 + col] + red[128 + col] + red[192 + col];
-            inv[n] = sum > 0.0f ? 1.0f / sum : 0.0f;
-          }
+          for (int n = 0; n < 16; n += 4)
+            *reinterpret_cast<float4*>(inv + n) = *reinterpret_cast<const float4*>(inv_s + n0 + n);
           for (int c = 0; c < p.nch; ++c) {
             const int lat = 128 * c + 32 * sp + lane;
             float o[16];
@@ -667,14 +701,11 @@ __global__ void __launch_bounds__(kBlockThreads<Q8>, 1)
               for (int n = 0; n < 16; ++n) o[n] = 0.0f;
             }
             if (lat < p.r) {
+              uint16_t* dst = out + int64_t(n0) * p.r + lat;
 #pragma unroll
               for (int n = 0; n < 16; ++n) {
-                const int col = n0 + n;
-                if (col < cols_here) {
-                  const float v = o[n] * inv[n];
-                  if (whole) p.o_latent[(row0 + col) * p.r + lat] = cvt_bf16(v);
-                  else p.part_o[(int64_t(pslot) * NCOL + col) * p.r + lat] = cvt_bf16(v);
-                }
+                if (n0 + n < cols_here) *dst = cvt_bf16(o[n] * inv[n]);
+                dst += p.r;
               }
             }
           }
