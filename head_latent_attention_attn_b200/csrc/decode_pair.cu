@@ -531,6 +531,8 @@ __global__ void __launch_bounds__(kThreads<Q8>, 1)
       const bool row_ok = row < p.qH;
       const float c_log2 = p.scale_log2;
       const bool vec_out = (reinterpret_cast<uintptr_t>(p.o_latent) & 15u) == 0;
+      const bool q_wide = (reinterpret_cast<uintptr_t>(p.q_ext) & 31u) == 0 && p.D % 16 == 0;
+      const bool vec32 = (reinterpret_cast<uintptr_t>(p.o_latent) & 31u) == 0;
       const int rpitch = rh * 2;                // bytes per Q rotary row in shared memory
       const bool tr = (sp == 0 && lane == 0);
       (void)tr;
@@ -548,20 +550,39 @@ __global__ void __launch_bounds__(kThreads<Q8>, 1)
       // zero rows past q*H. Ends with this warp's arrival on q_full (owners and senders).
       auto load_q = [&](int b) {
         const uint16_t* q = p.q_ext + (int64_t(b) * p.qH + row) * p.D;
-        for (int c0 = 0; c0 < rhalf; c0 += 32) {
-          const uint16_t* src = q + int(rank) * rhalf + c0 + 16 * qt;
-          uint32_t v[8];
-          if (row_ok) {
-            const uint4 a = *reinterpret_cast<const uint4*>(src);
-            const uint4 bb = *reinterpret_cast<const uint4*>(src + 8);
-            v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-            v[4] = bb.x; v[5] = bb.y; v[6] = bb.z; v[7] = bb.w;
-          } else {
+        // 64 columns at a time (rhalf is a multiple of 64), a step's loads one step ahead. Every
+        // lane reads its own row, so a load instruction visits 32 lines whatever its width: 32
+        // bytes where the rows start on 32-byte boundaries.
+        uint4 x[4];
+        auto fetch = [&](int c0) {
 #pragma unroll
-            for (int k = 0; k < 8; ++k) v[k] = 0u;
+          for (int i = 0; i < 4; i += 2) {
+            const uint16_t* src = q + int(rank) * rhalf + c0 + 16 * i + 16 * qt;
+            if (!row_ok) {
+              x[i] = x[i + 1] = make_uint4(0, 0, 0, 0);
+            } else if (q_wide) {
+              ld_global_v8(src, &x[i], &x[i + 1]);
+            } else {
+              x[i] = reinterpret_cast<const uint4*>(src)[0];
+              x[i + 1] = reinterpret_cast<const uint4*>(src)[1];
+            }
           }
-          if (c0 < kQTmem) tm_st_x8_s8(trow + kColQ + c0 / 2, v);
-          else store_qlat(qlat, n, c0 + 16 * qt - kQTmem, v);
+        };
+        fetch(0);
+        for (int c0 = 0; c0 < rhalf; c0 += 64) {
+          uint32_t v[2][8];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t* d = v[i / 2] + 4 * (i % 2);
+            d[0] = x[i].x; d[1] = x[i].y; d[2] = x[i].z; d[3] = x[i].w;
+          }
+          if (c0 + 64 < rhalf) fetch(c0 + 64);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int c = c0 + 32 * i;
+            if (c < kQTmem) tm_st_x8_s8(trow + kColQ + c / 2, v[i]);
+            else store_qlat(qlat, n, c + 16 * qt - kQTmem, v[i]);
+          }
         }
         for (int c = qt; c < rh / 8; c += 2) {
           const uint4 v = row_ok ? *reinterpret_cast<const uint4*>(q + r + int(rank) * rh + 8 * c)
@@ -605,7 +626,11 @@ __global__ void __launch_bounds__(kThreads<Q8>, 1)
         const int pslot = piece_slot(vc, w.s, per, p.col_groups, cg);
         const float inv = (lt > 0.0f && !aborted) ? 1.0f / lt : 0.0f;
         const int64_t lat0 = int64_t(rank) * rhalf + 16 * qt;   // this thread's 16 of every 32
-        for (int c0 = 0; c0 < rhalf; c0 += 32) {
+        // A partial's rows start on 16-byte boundaries (r % 8 == 0, lat0 + c0 a multiple of 16);
+        // a padding row past q*H has nothing to write.
+        uint16_t* dst = whole ? p.o_latent + grow * r + lat0
+                              : p.part_o + (int64_t(pslot) * kPairRows + n) * r + lat0;
+        for (int c0 = 0; c0 < rhalf; c0 += 32, dst += 32) {
           float o[16];
           if (!aborted) {
             tm_ld_x16_s16(trow + kColO + c0, o);
@@ -614,32 +639,21 @@ __global__ void __launch_bounds__(kThreads<Q8>, 1)
 #pragma unroll
             for (int c = 0; c < 16; ++c) o[c] = 0.0f;
           }
-          if (!row_ok) {
-            // padding row past q*H: nothing to write
-          } else if (whole) {
-            uint16_t* dst = p.o_latent + grow * r + lat0 + c0;
-            if (vec_out) {
+          if (!row_ok) continue;
+          if (!whole || vec_out) {
+            uint32_t x[8];
 #pragma unroll
-              for (int c = 0; c < 16; c += 8)
-                *reinterpret_cast<uint4*>(dst + c) =
-                    make_uint4(cvt_bf16x2(o[c] * inv, o[c + 1] * inv),
-                               cvt_bf16x2(o[c + 2] * inv, o[c + 3] * inv),
-                               cvt_bf16x2(o[c + 4] * inv, o[c + 5] * inv),
-                               cvt_bf16x2(o[c + 6] * inv, o[c + 7] * inv));
+            for (int c = 0; c < 8; ++c) x[c] = cvt_bf16x2(o[2 * c] * inv, o[2 * c + 1] * inv);
+            const uint4 lo = make_uint4(x[0], x[1], x[2], x[3]), hi = make_uint4(x[4], x[5], x[6], x[7]);
+            if (whole && !vec32) {
+              reinterpret_cast<uint4*>(dst)[0] = lo;
+              reinterpret_cast<uint4*>(dst)[1] = hi;
             } else {
-#pragma unroll
-              for (int c = 0; c < 16; ++c) dst[c] = f32_to_bf16_rne(o[c] * inv);
+              st_global_v8(dst, lo, hi);
             }
           } else {
-            // bf16 partial (16-byte aligned: r % 8 == 0 and lat0 + c0 a multiple of 16)
-            uint16_t* dst = p.part_o + (int64_t(pslot) * kPairRows + n) * r + lat0 + c0;
 #pragma unroll
-            for (int c = 0; c < 16; c += 8)
-              *reinterpret_cast<uint4*>(dst + c) =
-                  make_uint4(cvt_bf16x2(o[c] * inv, o[c + 1] * inv),
-                             cvt_bf16x2(o[c + 2] * inv, o[c + 3] * inv),
-                             cvt_bf16x2(o[c + 4] * inv, o[c + 5] * inv),
-                             cvt_bf16x2(o[c + 6] * inv, o[c + 7] * inv));
+            for (int c = 0; c < 16; ++c) dst[c] = f32_to_bf16_rne(o[c] * inv);
           }
         }
         tc_fence_before();

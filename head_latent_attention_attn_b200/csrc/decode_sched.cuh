@@ -104,7 +104,8 @@ MLA_DEVICE void find_tile_range(const DecodeParams& p, int vc, int vgrid, bool r
     if (lane == 31) warp_sum[warp] = incl;
     __syncthreads();
     int before = sched[5];
-    for (int w = 0; w < warp; ++w) before += warp_sum[w];
+    if (b0 + 32 * warp < p.batch)       // the others hold no sequence, and this is the last chunk
+      for (int w = 0; w < warp; ++w) before += warp_sum[w];
     const int start = before + incl - t;
     if (b < p.batch && start <= r0 && r0 < start + t) {
       sched[0] = b;

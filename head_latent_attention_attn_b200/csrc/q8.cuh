@@ -101,6 +101,15 @@ MLA_DEVICE uint4 ld_stream_v4(const void* p) {
   return v;
 }
 
+// 32 bytes of global memory, 32-byte aligned.
+MLA_DEVICE void ld_global_v8(const void* p, uint4* lo, uint4* hi) {
+  asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(lo->x), "=r"(lo->y), "=r"(lo->z), "=r"(lo->w), "=r"(hi->x), "=r"(hi->y),
+                 "=r"(hi->z), "=r"(hi->w)
+               : "l"(p)
+               : "memory");
+}
+
 // 32 bytes to global memory, 32-byte aligned: a whole sector of a line in one access.
 MLA_DEVICE void st_global_v8(void* p, const uint4& lo, const uint4& hi) {
   asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(lo.x),
