@@ -689,11 +689,10 @@ mla_status build_decode(const mla_dims* dims, const void* q_ext, const void* cac
 }
 
 // Where mla_decode_attn_q8 may put the contexts' rows in bf16 (behind them their block table), so
-// that each page is converted once and not by every block of query rows that reads it. On B200
-// the conversion in the decode kernel makes the two-CTA kernel 1.4 times slower (64 x 8192
-// tokens, 128 heads: 261 us, 188 us over bf16 rows), while a pass that writes the rows first
-// costs 0.75 of such a block's time; from three blocks on (off != 0) it pays: a chunk of 256
-// rows of 128 heads over 4096 tokens takes 530 us with 256 conversions of every page.
+// that each page is converted once and not by every block of query rows that reads it. A pass that
+// writes the rows first pays from three blocks on (off != 0). 8 x 4096 tokens on B200: three blocks
+// of the two-CTA kernel (128 heads, r 512) take 96 us in place and 86 converted first, eight 228 and
+// 180; three of the one-CTA kernel (64 heads, r 448) 66 and 62, eight 125 and 108.
 struct RowsPlan {
   size_t off, table_off, bytes;
   int32_t tiles;

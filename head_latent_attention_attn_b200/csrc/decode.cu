@@ -77,10 +77,10 @@ static_assert(kRegsIssue <= kRegsLaunch && kRegsDequant <= kRegsLaunch &&
 static_assert(kRegsIssue + kRegsSoftmax + (kDqWarps / 4) * kRegsDequant <=
                   (2 + kDqWarps / 4) * kRegsLaunch,
               "the groups' registers exceed what the block is launched with");
-// Dequantising warps at work. Four with two groups each where the softmax of 64 columns is what a
-// page waits for and there is little to convert: r <= 256 (1M tokens, 64 rows, r 256: 202 us, 214
-// with eight); eight otherwise (64 rows, r 512: 187 us, 200 with four; 16 rows, r 256: 129 us, 147;
-// 32 rows, r 512: 436 us, 465).
+// Dequantising warps at work. Four with two groups each where the softmax of 64 columns needs the
+// issue slots and there is little to convert: r <= 256 (1M tokens, 64 rows, r 256: 157 us, 161 with
+// eight; 64 x 8192 tokens: 83 us, 86); eight otherwise (16 rows over 1M tokens, r 256: 131 us, 145
+// with four).
 template <int NCOL>
 MLA_DEVICE int dequant_warps(int r) { return NCOL == 64 && r <= 4 * kQ8Cols ? 4 : kDqWarps; }
 template <bool Q8>
@@ -179,7 +179,9 @@ MLA_DEVICE void tmem_ld_s<32>(uint32_t taddr, float* v) {
 
 // Column values of 16 lanes joined by `op`, in the steps lane ^ 8, ^ 4, ^ 2, ^ 1; in each but for the
 // last of N = 8, a lane keeps half of its columns and hands over the others, so that all N columns
-// take 2 (N - 2) shuffles less than one at a time. Lane i (of 16) then holds the columns from
+// take N - 2 (N = 32) shuffles instead of 4 N. Every pair is joined as it would be one column at a
+// time, so sums keep their bits. For 64 columns a move of the reference takes 2,100 cycles of a
+// tile this way (8,700 one at a time). Lane i (of 16) then holds the columns from
 // joined_column<N>(i) on, N / 16 of them, in v[0], ...; with N = 8, two lanes hold each.
 template <int N, class Op>
 MLA_DEVICE void join16(float* v, int lane, Op op) {
