@@ -841,7 +841,6 @@ __global__ void __launch_bounds__(kThreads<Q8>, 1)
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&s_free[sb]);
-            if (t == te - 1 && w.s + w.tiles < r1) load_q(w.b + 1);
             uint32_t pw[kPackWords];
 #pragma unroll
             for (int g = 0; g < kHalfTok / 4; ++g) pack_f24(x + 4 * g, pw + 3 * g);
@@ -859,6 +858,9 @@ __global__ void __launch_bounds__(kThreads<Q8>, 1)
                             make_uint4(pw[4 * c], pw[4 * c + 1], pw[4 * c + 2], pw[4 * c + 3]), rb);
             }
             if (tr) MLA_PTRACE(4, jj);
+            // S of the piece's last tile is complete and on its way: the next piece's Q may replace
+            // this one (with the scores still in registers here they would spill)
+            if (t == te - 1 && w.s + w.tiles < r1) load_q(w.b + 1);
           }
         }
       } else {
