@@ -70,7 +70,7 @@ constexpr int kPvWarp = Q8 ? 2 : 6;
 template <bool Q8>
 constexpr int kSmWarp0 = Q8 ? 4 : 2;                 // first of the four softmax warps
 constexpr int kDqWarp0 = 8, kDqWarps = 8;
-constexpr int kRegsLaunch = 128, kRegsIssue = 72, kRegsSoftmax = 232, kRegsDequant = 104;
+constexpr int kRegsLaunch = 128, kRegsIssue = 72, kRegsSoftmax = 216, kRegsDequant = 112;
 // setmaxnreg may only lower a group's share by .dec and raise it by .inc
 static_assert(kRegsIssue <= kRegsLaunch && kRegsDequant <= kRegsLaunch &&
               kRegsSoftmax >= kRegsLaunch, "register shares");
@@ -79,7 +79,7 @@ static_assert(kRegsIssue + kRegsSoftmax + (kDqWarps / 4) * kRegsDequant <=
               "the groups' registers exceed what the block is launched with");
 // Dequantising warps at work. Four with two groups each where the softmax of 64 columns needs the
 // issue slots and there is little to convert: r <= 256 (1M tokens, 64 rows, r 256: 157 us, 161 with
-// eight; 64 x 8192 tokens: 83 us, 86); eight otherwise (16 rows over 1M tokens, r 256: 131 us, 145
+// eight; 64 x 8192 tokens: 83 us, 86); eight otherwise (16 rows over 1M tokens, r 256: 127 us, 145
 // with four).
 template <int NCOL>
 MLA_DEVICE int dequant_warps(int r) { return NCOL == 64 && r <= 4 * kQ8Cols ? 4 : kDqWarps; }

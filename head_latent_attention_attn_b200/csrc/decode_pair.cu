@@ -80,8 +80,11 @@ constexpr int kRowWarp0 = Q8 ? 4 : 3;
 constexpr int kDqWarp0 = kRowWarp0<true> + 12, kDqWarps = 8;
 template <bool Q8>
 constexpr int kThreads = 32 * (Q8 ? kDqWarp0 + kDqWarps : kRowWarp0<Q8> + 12);
-constexpr int kRegsLaunch = 80, kRegsIssue = 56, kRegsOwner = 128, kRegsSender = 88,
-              kRegsReceiver = 88, kRegsDequant = 56;
+// The owners hold most; the issuers' and the senders' loops are as fast with what the block was
+// launched with (64 x 8192 tokens of 128 heads: 237 us; 257 with 56 for the issuers and 88 for the
+// senders and receivers, 263 with 48 for the dequantising warps and 144 for the owners).
+constexpr int kRegsLaunch = 80, kRegsIssue = 80, kRegsOwner = 128, kRegsSender = 80,
+              kRegsReceiver = 80, kRegsDequant = 56;
 // setmaxnreg may only lower a group's share by .dec and raise it by .inc
 static_assert(kRegsIssue <= kRegsLaunch && kRegsDequant <= kRegsLaunch &&
               kRegsOwner >= kRegsLaunch && kRegsSender >= kRegsLaunch &&

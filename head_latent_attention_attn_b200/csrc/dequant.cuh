@@ -9,9 +9,9 @@
 //
 // What this costs is issue slots, which the softmax warps of the same SM need: some 12 cycles of
 // a scheduler for 4 codes of a warp. Against the bf16 cache the one-CTA kernel keeps its time, for
-// 0.56 to 0.61 of the bytes (16 rows over 1M tokens 131 us, 121 over bf16; 128 ragged sequences of
-// 32 heads 402 and 390; 64 rows over 1M tokens 158 and 137, over 64 x 8192 of r 512 140 and 132);
-// the two-CTA kernel takes 1.45 times (267 and 182 us). Measured and slower: 16 warps of half the
+// 0.56 to 0.61 of the bytes (16 rows over 1M tokens 127 us, 121 over bf16; 128 ragged sequences of
+// 32 heads 402 and 390; 64 rows over 1M tokens 158 and 137, over 64 x 8192 of r 512 139 and 132);
+// the two-CTA kernel takes 1.3 times (237 and 181 us). Measured and slower: 16 warps of half the
 // blocks, two pages ahead in registers, converting before the slot is free, S^T begun on half a
 // page, PV by latent chunk so that the slot's first blocks are free early.
 #pragma once
