@@ -205,10 +205,17 @@ MLA_DEVICE uint2 ld_shared_v2(uint32_t saddr) {
 
 // Four 24-bit values (fp32 rounded to sign, exponent and a 15-bit mantissa) in three words
 // (value k's three bytes follow value k-1's), and back to fp32 with a zero low byte.
-// Rounding adds half of the dropped byte; the byte moves are single byte permutes.
+// Rounding adds half of the dropped byte; the byte moves are single byte permutes. That addition
+// would carry a NaN (all mantissa bits set, as the tensor core makes it) into the sign and hand the
+// partner a score of -0. So a NaN goes as +inf, of which the row's softmax makes NaN again where the
+// row sees the token: one fp32 minimum a score (256 rows of 128 heads over 4096 tokens: 372 -> 380 us,
+// 64 x 8192 tokens over the 8-bit cache 241 -> 241.5; looking for a NaN by the sum of a row's scores
+// first took 379 to 390 and 246 to 271).
+MLA_DEVICE uint32_t f24_bits(float x) {
+  return __float_as_uint(fminf(x, __uint_as_float(0x7F800000u))) + 0x80u;
+}
 MLA_DEVICE void pack_f24(const float* v, uint32_t* w) {
-  const uint32_t a = __float_as_uint(v[0]) + 0x80u, b = __float_as_uint(v[1]) + 0x80u;
-  const uint32_t c = __float_as_uint(v[2]) + 0x80u, d = __float_as_uint(v[3]) + 0x80u;
+  const uint32_t a = f24_bits(v[0]), b = f24_bits(v[1]), c = f24_bits(v[2]), d = f24_bits(v[3]);
   w[0] = __byte_perm(a, b, 0x5321);   // a1 a2 a3 b1
   w[1] = __byte_perm(b, c, 0x6532);   // b2 b3 c1 c2
   w[2] = __byte_perm(c, d, 0x7653);   // c3 d1 d2 d3
