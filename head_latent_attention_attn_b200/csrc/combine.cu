@@ -1,7 +1,9 @@
 // combine.cu - the merge of sequences cut between CTAs by mla_decode_attn's schedule: each
 // piece left its normalised partial o (bf16) and lse (fp32); the row's
 //   lse = log sum_i e^{lse_i},   o = sum_i e^{lse_i - lse} o_i
-// (the log-sum-exp identity) is written to o_latent and lse.
+// (the log-sum-exp identity) is written to o_latent and lse. A piece whose row saw no token has
+// lse_i = -inf and is left out; one with a NaN lse_i makes the row NaN (the maximum passes over it,
+// the sum of the exponentials does not).
 #include <math.h>
 
 #include <algorithm>
@@ -68,7 +70,7 @@ __global__ void __launch_bounds__(128) mla_combine_kernel(const CombineParams p)
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
-    if (lane == 0) lse_s = mx == -INFINITY ? -INFINITY : mx + logf(den);
+    if (lane == 0) lse_s = den == 0.0f ? -INFINITY : mx + logf(den);
   }
   __syncthreads();
   const float lse = lse_s;
@@ -180,7 +182,7 @@ __global__ void __launch_bounds__(256) mla_combine_rows_kernel(const CombinePara
       float den = my_l == -INFINITY ? 0.0f : expf(my_l - mx);
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
-      lse = mx == -INFINITY ? -INFINITY : mx + logf(den);
+      lse = den == 0.0f ? -INFINITY : mx + logf(den);
 #pragma unroll
       for (int i = 0; i < kFewPieces; ++i) {
         const float li = __shfl_sync(0xffffffffu, my_l, i);
@@ -206,7 +208,7 @@ __global__ void __launch_bounds__(256) mla_combine_rows_kernel(const CombinePara
       }
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
-      lse = mx == -INFINITY ? -INFINITY : mx + logf(den);
+      lse = den == 0.0f ? -INFINITY : mx + logf(den);
       for (int i = i0; i <= i1; ++i) {
         const int64_t sl = piece_slot(i, s, per, G, cg);
         const float li = p.part_lse[sl * p.ncol + n];

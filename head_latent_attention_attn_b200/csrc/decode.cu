@@ -675,9 +675,10 @@ __global__ void __launch_bounds__(kBlockThreads<Q8>, 1)
         float* inv_s = alpha_s;   // 1 / sum of every column
         if (tid < NCOL) {
           const float sum = red[tid] + red[64 + tid] + red[128 + tid] + red[192 + tid];
-          inv_s[tid] = sum > 0.0f ? 1.0f / sum : 0.0f;
+          // a row that sees nothing has a sum of 0; a NaN stays NaN in o and lse
+          inv_s[tid] = sum != 0.0f ? 1.0f / sum : 0.0f;
           const float lse =
-              (sum > 0.0f && !aborted) ? (mref_s[tid] + __log2f(sum)) * kLn2 : -INFINITY;
+              (sum != 0.0f && !aborted) ? (mref_s[tid] + __log2f(sum)) * kLn2 : -INFINITY;
           if (tid < cols_here) {
             if (whole) p.lse[row0 + tid] = lse;
             else p.part_lse[int64_t(pslot) * NCOL + tid] = lse;

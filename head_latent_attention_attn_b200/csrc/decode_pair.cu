@@ -634,7 +634,8 @@ __global__ void __launch_bounds__(kThreads<Q8>, 1)
         const bool whole = (tb == w.s) && (te == w.s + w.tiles);
         const int64_t grow = int64_t(w.b) * p.qH + row;   // global (b, i, h) row
         const int pslot = piece_slot(vc, w.s, per, p.col_groups, cg);
-        const float inv = (lt > 0.0f && !aborted) ? 1.0f / lt : 0.0f;
+        // a row that sees nothing has a sum of 0; a NaN stays NaN in o and lse
+        const float inv = (lt != 0.0f && !aborted) ? 1.0f / lt : 0.0f;
         const int64_t lat0 = int64_t(rank) * rhalf + 16 * qt;   // this thread's 16 of every 32
         // A partial's rows start on 16-byte boundaries (r % 8 == 0, lat0 + c0 a multiple of 16);
         // a padding row past q*H has nothing to write.
@@ -816,7 +817,7 @@ __global__ void __launch_bounds__(kThreads<Q8>, 1)
           bool aborted = false;
           write_o(w, tb, te, jj - 1, lt, &aborted);
           if (row_ok && qt == 0) {
-            const float lse = (lt > 0.0f && !aborted) ? (mref + __log2f(lt)) * kLn2 : -INFINITY;
+            const float lse = (lt != 0.0f && !aborted) ? (mref + __log2f(lt)) * kLn2 : -INFINITY;
             const bool whole = (tb == w.s) && (te == w.s + w.tiles);
             if (whole) p.lse[int64_t(w.b) * p.qH + row] = lse;
             else

@@ -45,3 +45,21 @@ def test_a_bad_block_in_either_latent_half_reaches_every_row(name, col, monkeypa
         assert bool(torch.isfinite(o0.float()).all())
         assert bool(torch.isnan(o[0].float()).all())
         assert torch.equal(o[1], o0[1]) and torch.equal(lse[1], lse0[1])
+
+
+@pytest.mark.parametrize("ns", [1, 3, 7, 20])
+@pytest.mark.parametrize("name,q", [("hybrid", 1), ("qwen3_30b_a3b", 1), ("rows_64", 1), ("deepseek_v2", 1),
+                                    ("pair_r256", 3)])
+def test_a_bad_block_is_not_lost_with_its_piece(name, q, ns):
+    """One context of 20 pages held whole, in 3 pieces (merged a warp a row), 7 and 20 (a block a row):
+    a bad block in one of the pieces, then in every page, makes o and lse NaN whatever the cut."""
+    f = Filled(name, [1280], seed=2)
+    q_bits = f.query(q)
+    for o, lse in both(f, q_bits, ns):
+        assert bool(torch.isfinite(o.float()).all()) and bool(torch.isfinite(lse).all())
+    poison(f, 0, 700, 3)
+    for _ in range(2):
+        for o, lse in both(f, q_bits, ns):
+            assert bool(torch.isnan(lse).all()) and bool(torch.isnan(o.float()).all())
+        for page in range(20):
+            poison(f, 0, 64 * page, 60, INF)
