@@ -222,7 +222,9 @@ size_t decode_smem_bytes(int ncol, int nblk, int slot_blocks, int nslot, int npt
   return decode_layout(ncol, nblk, slot_blocks, nslot, npt).total;
 }
 
-template <int NCOL, bool Q8>
+// kHide: some rows of a block may not see a token that others see, or (bf16 cache) a page may hold
+// more than the context.
+template <int NCOL, bool Q8, bool kHide>
 __global__ void __launch_bounds__(kBlockThreads<Q8>, 1)
     mla_decode_kernel(const __grid_constant__ DecodeParams p) {
   constexpr int HALF = NCOL / 2;
@@ -462,12 +464,13 @@ __global__ void __launch_bounds__(kBlockThreads<Q8>, 1)
     if constexpr (Q8) reg_dec<kRegsDequant>();
     if (has_work) {
       const int wi = warp - kDqWarp0, lb = p.r / kQ8Cols;
+      const int hidden = RowsSeen(p, cg, NCOL).hidden_all;
       if (dequant_warps<NCOL>(p.r) == 4) {
         if (wi < 4)
-          dequant_pages<4, 2>(p, cg, r0, r1, sched[0], sched[1], wi, 0, lb, slots, slot_bytes, full,
-                              empty, wc);
+          dequant_pages<4, 2>(p, cg, r0, r1, sched[0], sched[1], wi, 0, lb, hidden, slots, slot_bytes,
+                              full, empty, wc);
       } else {
-        dequant_pages<kQ8MaxBlocks, 1>(p, cg, r0, r1, sched[0], sched[1], wi, 0, lb, slots,
+        dequant_pages<kQ8MaxBlocks, 1>(p, cg, r0, r1, sched[0], sched[1], wi, 0, lb, hidden, slots,
                                        slot_bytes, full, empty, wc);
       }
     }
@@ -484,6 +487,7 @@ __global__ void __launch_bounds__(kBlockThreads<Q8>, 1)
       const int c0 = hf * HALF;                 // first column of this thread
       const bool col_owner = (lane & 15) == 0;  // publishes its half-warp's column values
       const float c_log2 = p.scale_log2;
+      const RowsSeen seen_by(p, cg, NCOL);
 
       UnitWalk w{sched[0], sched[1]};
       int jj = 0;
@@ -636,15 +640,16 @@ __global__ void __launch_bounds__(kBlockThreads<Q8>, 1)
                   packed[ch * 4 + 0], packed[ch * 4 + 1], packed[ch * 4 + 2], packed[ch * 4 + 3]);
             }
           }
-          // cache rows past the context may hold anything (even NaN): zero them so that
-          // 0-weight x garbage cannot reach O^T
-          if (!Q8 && pos >= L) {
-            uint8_t* sbase = slots + slot * slot_bytes;
-            for (int k = hf; k < 2 * p.nch; k += 2) {
-              uint4* rowp = reinterpret_cast<uint4*>(sbase + k * kBlkBytes + tok * 128);
-#pragma unroll
-              for (int ch = 0; ch < 8; ++ch) rowp[ch] = make_uint4(0, 0, 0, 0);
-            }
+          // a token that some row does not see, or past the context, where a page may hold anything
+          // (over the 8-bit cache what no row sees is zero from the conversion on). The code
+          // alone costs there (4 rows of 16 heads over 16 x 64K tokens 147 us instead of 143, 2 of 28
+          // heads over 64 x 4096 51 instead of 47), so that blocks of rows which see the same tokens
+          // have an instance without it (kHide).
+          if (kHide && ragged && pos >= L - seen_by.hidden_some && !(Q8 && pos >= L - seen_by.hidden_all)) {
+            (void)mbar_try_wait(&full[slot], ring.round & 1);   // long complete: the page's bytes
+            uint8_t* row = slots + slot * slot_bytes + tok * 128;
+            for (int k = hf; k < (p.r + 63) / 64; k += 2)
+              hide_token(row + k * kBlkBytes, pos >= L - seen_by.hidden_all, lane);
           }
           // P^T(j) and the zeroed rows are complete: hand the page to the PV issuer
           fence_proxy_async_smem();
@@ -731,34 +736,35 @@ extern "C" int mla_trace_read(unsigned long long* host, int n) {
 #endif
 
 
-template <int NCOL, bool Q8>
+template <int NCOL, bool Q8, bool kHide>
 static cudaError_t launch_decode_n(const DecodeParams& p, dim3 grid, size_t smem,
                                    cudaStream_t stream) {
   if (Q8) {
     static std::atomic<bool> known{false};
-    const cudaError_t e = check_launch_regs(mla_decode_kernel<NCOL, Q8>, kRegsLaunch, &known);
+    const cudaError_t e = check_launch_regs(mla_decode_kernel<NCOL, Q8, kHide>, kRegsLaunch, &known);
     if (e != cudaSuccess) return e;
   }
-  cudaError_t e = cudaFuncSetAttribute(mla_decode_kernel<NCOL, Q8>,
+  cudaError_t e = cudaFuncSetAttribute(mla_decode_kernel<NCOL, Q8, kHide>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
   if (e != cudaSuccess) return e;
-  return launch_pdl(mla_decode_kernel<NCOL, Q8>, grid, dim3(kBlockThreads<Q8>), smem, stream,
+  return launch_pdl(mla_decode_kernel<NCOL, Q8, kHide>, grid, dim3(kBlockThreads<Q8>), smem, stream,
                     1, p);
+}
+
+template <int NCOL>
+static cudaError_t launch_decode_c(const DecodeParams& p, dim3 grid, size_t smem,
+                                   cudaStream_t stream) {
+  if (!p.cache_q8) return launch_decode_n<NCOL, false, true>(p, grid, smem, stream);
+  return same_rows_seen(p, NCOL) ? launch_decode_n<NCOL, true, false>(p, grid, smem, stream)
+                                 : launch_decode_n<NCOL, true, true>(p, grid, smem, stream);
 }
 
 cudaError_t launch_decode(const DecodeParams& p, int ncol, dim3 grid, size_t smem,
                           cudaStream_t stream) {
-  const bool q8 = p.cache_q8 != nullptr;
   switch (ncol) {
-    case 16:
-      return q8 ? launch_decode_n<16, true>(p, grid, smem, stream)
-                : launch_decode_n<16, false>(p, grid, smem, stream);
-    case 32:
-      return q8 ? launch_decode_n<32, true>(p, grid, smem, stream)
-                : launch_decode_n<32, false>(p, grid, smem, stream);
-    case 64:
-      return q8 ? launch_decode_n<64, true>(p, grid, smem, stream)
-                : launch_decode_n<64, false>(p, grid, smem, stream);
+    case 16: return launch_decode_c<16>(p, grid, smem, stream);
+    case 32: return launch_decode_c<32>(p, grid, smem, stream);
+    case 64: return launch_decode_c<64>(p, grid, smem, stream);
     default: return cudaErrorInvalidValue;
   }
 }

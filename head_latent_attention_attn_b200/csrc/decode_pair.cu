@@ -25,16 +25,16 @@
 // the others). With P in its own buffers, S of tile j + 2 waits only until the scores of
 // tile j have been read, not for PV of tile j.
 //
-// Roles (480 threads): warp 0 TMA producer, warp 1 S issuer and TMEM owner, warp 2 PV
-// issuer, warps 3-14 the rows. TMEM lane n holds row n and a warp reaches only the 32 lanes
+// Roles (512 threads): warp 0 TMA producer, warp 1 S issuer and TMEM owner, warp 2 PV
+// issuer, warp 3 what some rows do not see, warps 4-15 the rows. TMEM lane n holds row n and a warp reaches only the 32 lanes
 // of its sub-partition (warp % 4). CTA k owns the rows on lanes 16k..16k+15 of every
 // sub-partition, so each of the three row roles has one warp on every SM sub-partition
 // (its issue slots and MUFU units). With 16x32bx2 TMEM accesses a warp covers 16 lanes,
 // two threads per row (lanes i and i + 16: tokens 0-31 and 32-63):
-//   owners    (warps 3-6, this CTA's rows): combine the two partials, softmax, P, the
+//   owners    (warps 4-7, this CTA's rows): combine the two partials, softmax, P, the
 //              epilogue and lse of the own rows;
-//   senders   (warps 7-10, the partner's rows): read their partial scores and send them;
-//   receivers (warps 11-14, the partner's rows): take the partner's P and rescale factors
+//   senders   (warps 8-11, the partner's rows): read their partial scores and send them;
+//   receivers (warps 12-15, the partner's rows): take the partner's P and rescale factors
 //              for those rows into TMEM, and their epilogue.
 #include <math.h>
 
@@ -70,16 +70,15 @@ __device__ unsigned long long g_mla_pair_trace[kPairTraceEvents * kPairTraceTile
 
 namespace {
 
-constexpr int kPvWarp = 2;
+constexpr int kPvWarp = 2, kHideWarp = 3;
 // First of the 12 row warps. Over the 8-bit cache (Q8) eight more warps follow them, which
-// dequantise this CTA's half of each page, one per 8-token group, and the row warps start at 4
-// so that every role is an aligned group of four warps and can take its own share of the
-// registers (80 a thread at launch, 480 over the six groups).
+// dequantise this CTA's half of each page, one per 8-token group. Every role but the first four
+// warps' is an aligned group of four, so that it can take its own share of the registers there
+// (80 a thread at launch, 480 over the six groups).
+constexpr int kRowWarp0 = 4;
+constexpr int kDqWarp0 = kRowWarp0 + 12, kDqWarps = 8;
 template <bool Q8>
-constexpr int kRowWarp0 = Q8 ? 4 : 3;
-constexpr int kDqWarp0 = kRowWarp0<true> + 12, kDqWarps = 8;
-template <bool Q8>
-constexpr int kThreads = 32 * (Q8 ? kDqWarp0 + kDqWarps : kRowWarp0<Q8> + 12);
+constexpr int kThreads = 32 * (kDqWarp0 + (Q8 ? kDqWarps : 0));
 // The owners hold most; the issuers' and the senders' loops are as fast with what the block was
 // launched with (64 x 8192 tokens of 128 heads: 237 us; 257 with 56 for the issuers and 88 for the
 // senders and receivers, 263 with 48 for the dequantising warps and 144 for the owners).
@@ -115,7 +114,7 @@ __host__ __device__ inline uint32_t round_up_p(uint32_t x, uint32_t a) {
   return (x + a - 1) / a * a;
 }
 
-__host__ __device__ constexpr int pair_bars(int nslot) { return 2 * nslot + 16; }
+__host__ __device__ constexpr int pair_bars(int nslot) { return 4 * nslot + 15; }
 
 __host__ __device__ inline PairLayout pair_layout(int r, int rope_half, int nslot) {
   PairLayout L;
@@ -278,7 +277,9 @@ size_t decode_pair_smem_bytes(int r, int rope_half, int nslot) {
   return pair_layout(r, rope_half, nslot).total;
 }
 
-template <bool Q8>
+// kHide: some rows of a block may not see a token that others see, or (bf16 cache) a page may hold
+// more than the context: see kHideWarp.
+template <bool Q8, bool kHide>
 __global__ void __launch_bounds__(kThreads<Q8>, 1)
     mla_decode_pair_kernel(const __grid_constant__ DecodeParams p) {
   extern __shared__ uint8_t smem_raw[];
@@ -310,6 +311,9 @@ __global__ void __launch_bounds__(kThreads<Q8>, 1)
   uint64_t* xs_free = xs_full + 2;                     // [2] partner consumed ours
   uint64_t* xp_full = xs_free + 2;                     // partner's P landed
   uint64_t* xp_free = xp_full + 1;                     // partner consumed our P
+  // tiles with tokens to hide (kHide; each barrier's phases count only those):
+  uint64_t* hide_s = xp_free + 1;                      // [slot] S computed
+  uint64_t* hide_done = hide_s + p.nslot;              // [slot] tokens hidden, for PV
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -326,6 +330,8 @@ __global__ void __launch_bounds__(kThreads<Q8>, 1)
     for (int s = 0; s < p.nslot; ++s) {
       mbar_init(&full[s], Q8 ? 1 + kDqWarps : 1);
       mbar_init(&empty[s], 1);
+      mbar_init(&hide_s[s], 1);
+      mbar_init(&hide_done[s], 1);
     }
     mbar_init(q_full, 8);                              // 4 owner + 4 sender warps
     for (int i = 0; i < 2; ++i) {
@@ -367,7 +373,7 @@ __global__ void __launch_bounds__(kThreads<Q8>, 1)
     g_mla_pair_trace[kPairTraceEvents * kPairTraceTiles + 2 * blockIdx.x] = globaltimer_ns();
 #endif
 
-  const bool issuer = warp < kRowWarp0<Q8>;
+  const bool issuer = warp < kRowWarp0;
   if (issuer) {
     if constexpr (Q8) reg_dec<kRegsIssue>();
     if (warp == 0) {
@@ -437,6 +443,7 @@ __global__ void __launch_bounds__(kThreads<Q8>, 1)
         for (; ok && w.s < r1; w.s += w.tiles, ++w.b, ++pc) {
           w.load(p, cg);
           const int tb = max(w.s, r0), te = min(w.s + w.tiles, r1);
+          const int hide_t = kHide ? RowsSeen(p, cg, kPairRows).first_tile(w) : te;
           if (!mbar_wait(q_full, pc & 1, wc)) { ok = false; break; }
           tc_fence_after();
           for (int t = tb; ok && t < te; ++t, ++jj, ring.next()) {
@@ -476,6 +483,7 @@ __global__ void __launch_bounds__(kThreads<Q8>, 1)
                 umma_bf16(dS, ad, rd, idesc_s, 1u);
             }
             umma_commit(&s_full[sb]);
+            if (kHide && t >= hide_t) umma_commit(&hide_s[slot]);
             MLA_PTRACE(2, jj);
           }
         }
@@ -489,14 +497,21 @@ __global__ void __launch_bounds__(kThreads<Q8>, 1)
         const uint64_t pb0 = make_sdesc(smem_u32(slots), kBlk, 1024, kSw128);
         UnitWalk w{sched[0], sched[1]};
         int jj = 0;
+        uint32_t phases = 0;                 // bit s: of hide_done[s]
         SlotRing ring(p.nslot);
         bool ok = true;
         for (; ok && w.s < r1; w.s += w.tiles, ++w.b) {
           w.load(p, cg);
           const int tb = max(w.s, r0), te = min(w.s + w.tiles, r1);
+          const int hide_t = kHide ? RowsSeen(p, cg, kPairRows).first_tile(w) : te;
           for (int t = tb; t < te; ++t, ++jj, ring.next()) {
             const int sb = jj & 1;
             if (!mbar_wait(&p_full[sb], (jj >> 1) & 1, wc)) { ok = false; break; }
+            if (kHide && t >= hide_t) {
+              ok = mbar_wait(&hide_done[ring.slot], (phases >> ring.slot) & 1, wc);
+              if (!ok) break;
+              phases ^= 1u << ring.slot;
+            }
             tc_fence_after();
             // the first tile of a piece overwrites O: the previous piece's epilogue read O
             // before its warps arrived on p_full for this tile
@@ -514,14 +529,51 @@ __global__ void __launch_bounds__(kThreads<Q8>, 1)
         }
       }
       __syncwarp();
+    } else if (kHide && warp == kHideWarp && has_work) {
+      // ========================== tokens that some row does not see ========================
+      // Once S of a tile has been computed, such a token's latent half loses what a weight of 0 must
+      // not meet (see hide_token); over the bf16 cache what lies past the context is zeroed here too.
+      // Only these tiles wait for this warp. The same code in the owners' loop costs every tile,
+      // whether it runs or not (64 x 8192 tokens over the 8-bit cache 252 to 293 us instead of 239).
+      // This warp's hand-overs still cost 11 % there (4 rows of 32 heads, 64 x 4096 tokens: 148 us
+      // instead of 133), so that blocks of rows which see the same tokens have an instance without.
+      const RowsSeen seen(p, cg, kPairRows);
+      UnitWalk w{sched[0], sched[1]};
+      int jj0 = 0;                           // tiles before this piece
+      uint32_t phases = 0;                   // bit s: of hide_s[s]
+      bool ok = true;
+      for (; ok && w.s < r1; w.s += w.tiles, ++w.b) {
+        w.load(p, cg);
+        const int tb = max(w.s, r0), te = min(w.s + w.tiles, r1);
+        for (int t = max(tb, seen.first_tile(w)); t < te; ++t) {
+          const int jj = jj0 + (t - tb), slot = jj % p.nslot;
+          ok = __all_sync(0xffffffffu, mbar_wait(&hide_s[slot], (phases >> slot) & 1, wc));
+          if (!ok) break;
+          phases ^= 1u << slot;
+          (void)mbar_try_wait(&full[slot], (jj / p.nslot) & 1);   // long complete: the page's bytes
+          uint8_t* rows = slots + slot * lay.slot_bytes;
+          for (int i = lane; i < kDecodeTok; i += 32) {
+            const int pos = (t - w.s) * kDecodeTok + i;
+            const bool none = pos >= w.L - seen.hidden_all;
+            if (pos >= w.L - seen.hidden_some && !(Q8 && none))   // (zeros from the conversion on)
+              for (int k = 0; k < lb; ++k) hide_token(rows + k * kBlk + i * 128, none, lane);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&hide_done[slot]);
+        }
+        jj0 += te - tb;
+      }
+      __syncwarp();
     }
   } else if (Q8 && warp >= kDqWarp0) {
     // ============================== dequantising warps (Q8) ==============================
     if constexpr (Q8) reg_dec<kRegsDequant>();
     if (has_work)
       dequant_pages<kQ8MaxBlocks / 2, 1>(p, cg, r0, r1, sched[0], sched[1], warp - kDqWarp0,
-                                         int(rank) * lb, lb, slots, lay.slot_bytes, full, empty,
-                                         wc);
+                                         int(rank) * lb, lb,
+                                         RowsSeen(p, cg, kPairRows).hidden_all, slots,
+                                         lay.slot_bytes, full, empty, wc);
   } else if (has_work) {
     auto rows = [&](auto role_tag) {
       constexpr int role = decltype(role_tag)::value;   // 0 owner, 1 sender, 2 receiver
@@ -677,18 +729,15 @@ __global__ void __launch_bounds__(kThreads<Q8>, 1)
         UnitWalk w{sched[0], sched[1]};
         w.load(p, cg);
         int jj = 0;
-        SlotRing ring(p.nslot);
         while (true) {
           const int tb = max(w.s, r0), te = min(w.s + w.tiles, r1);
           const int L = w.L;
           // last position row n sees (causal: L - q + i); rows past q*H see L - 1
           const int lim = min(L - 1, p.causal ? L - p.q_len + qi : L - 1);
           float mref = kRefInit, l = 0.0f, lt = 0.0f;   // the same in both threads of a row
-          for (int t = tb; t < te; ++t, ++jj, ring.next()) {
+          for (int t = tb; t < te; ++t, ++jj) {
             const int sb = jj & 1;                 // S buffer and partial buffer of this tile
-            const int slot = ring.slot;
-            const int tile_pos0 = (t - w.s) * kDecodeTok;
-            const int pos0 = tile_pos0 + qt * kHalfTok;   // first token of this thread's half
+            const int pos0 = (t - w.s) * kDecodeTok + qt * kHalfTok;   // first token of this half
             // ---- own partial scores ----
             float s[kHalfTok];
             const bool got = __all_sync(0xffffffffu, mbar_wait(&s_full[sb], (jj >> 1) & 1, wc));
@@ -792,23 +841,8 @@ __global__ void __launch_bounds__(kThreads<Q8>, 1)
                             make_uint2(__float_as_uint(alpha), __float_as_uint(lt)), xp_full_r);
             }
             if (tr) MLA_PTRACE(6, jj);
-            // cache rows past the context may hold anything (even NaN): zero their latent half
-            // so that 0-weight x garbage cannot reach O
-            if (!Q8 && tile_pos0 + kDecodeTok > L) {
-              const int tid = sp * 32 + lane;      // 0..127
-              const int tok = tid & (kDecodeTok - 1);
-              if (tile_pos0 + tok >= L) {
-                uint8_t* sbase = slots + slot * lay.slot_bytes;
-                for (int k = tid >> 6; k < lb; k += 2) {
-                  uint4* rowp = reinterpret_cast<uint4*>(sbase + k * kBlk + tok * 128);
-#pragma unroll
-                  for (int ch = 0; ch < 8; ++ch) rowp[ch] = make_uint4(0, 0, 0, 0);
-                }
-              }
-            }
-            // P (and any O rescale and zeroed rows) complete: hand the tile to the PV issuer
+            // P (and any O rescale) complete: hand the tile to the PV issuer
             tmem_wait_st();
-            fence_proxy_async_smem();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&p_full[sb]);
@@ -932,7 +966,7 @@ __global__ void __launch_bounds__(kThreads<Q8>, 1)
         }
       }
     };
-    const int role = (warp - kRowWarp0<Q8>) >> 2;
+    const int role = (warp - kRowWarp0) >> 2;
     if (role == 0) {
       if constexpr (Q8) reg_inc<kRegsOwner>();
       rows(std::integral_constant<int, 0>{});
@@ -966,7 +1000,7 @@ extern "C" int mla_pair_trace_read(unsigned long long* host, int n) {
 
 int decode_pair_max_clusters(size_t smem) {
   // one CTA per SM by its shared memory, over either cache
-  if (cudaFuncSetAttribute(mla_decode_pair_kernel<false>,
+  if (cudaFuncSetAttribute(mla_decode_pair_kernel<false, true>,
                            cudaFuncAttributeMaxDynamicSharedMemorySize,
                            int(smem)) != cudaSuccess) {
     cudaGetLastError();
@@ -984,31 +1018,32 @@ int decode_pair_max_clusters(size_t smem) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   int n = 0;
-  if (cudaOccupancyMaxActiveClusters(&n, mla_decode_pair_kernel<false>, &cfg) != cudaSuccess) {
+  if (cudaOccupancyMaxActiveClusters(&n, mla_decode_pair_kernel<false, true>, &cfg) != cudaSuccess) {
     cudaGetLastError();
     return 0;
   }
   return n;
 }
 
-template <bool Q8>
+template <bool Q8, bool kHide>
 static cudaError_t launch_decode_pair_t(const DecodeParams& p, dim3 grid, size_t smem,
                                         cudaStream_t stream) {
   if (Q8) {
     static std::atomic<bool> known{false};
-    const cudaError_t e = check_launch_regs(mla_decode_pair_kernel<Q8>, kRegsLaunch, &known);
+    const cudaError_t e = check_launch_regs(mla_decode_pair_kernel<Q8, kHide>, kRegsLaunch, &known);
     if (e != cudaSuccess) return e;
   }
-  cudaError_t e = cudaFuncSetAttribute(mla_decode_pair_kernel<Q8>,
+  cudaError_t e = cudaFuncSetAttribute(mla_decode_pair_kernel<Q8, kHide>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
   if (e != cudaSuccess) return e;
-  return launch_pdl(mla_decode_pair_kernel<Q8>, grid, dim3(kThreads<Q8>), smem, stream, 2, p);
+  return launch_pdl(mla_decode_pair_kernel<Q8, kHide>, grid, dim3(kThreads<Q8>), smem, stream, 2, p);
 }
 
 cudaError_t launch_decode_pair(const DecodeParams& p, dim3 grid, size_t smem,
                                cudaStream_t stream) {
-  return p.cache_q8 ? launch_decode_pair_t<true>(p, grid, smem, stream)
-                    : launch_decode_pair_t<false>(p, grid, smem, stream);
+  if (!p.cache_q8) return launch_decode_pair_t<false, true>(p, grid, smem, stream);
+  return same_rows_seen(p, kPairRows) ? launch_decode_pair_t<true, false>(p, grid, smem, stream)
+                                      : launch_decode_pair_t<true, true>(p, grid, smem, stream);
 }
 
 }  // namespace mla

@@ -72,13 +72,14 @@ MLA_DEVICE void prefetch_pages(const DecodeParams& p, int cg, int r1, int upto,
 // All pages of tiles [r0, r1), whose first is of sequence b, which starts at tile s. This warp
 // converts the NG 8-token groups from NG * grp on of the page's column blocks [blk0, blk0 + nb),
 // nb <= NB, into the slot's blocks 0, 1, ... It waits for empty[slot] and arrives on full[slot]
-// once.
+// once. The last `hidden` tokens of a context, which none of the block's rows sees, become zeros.
 template <int NB, int NG>
 MLA_DEVICE void dequant_pages(const DecodeParams& p, int cg, int r0, int r1, int b, int s, int grp,
-                              int blk0, int nb, uint8_t* slots, uint32_t slot_bytes,
-                              uint64_t* full, uint64_t* empty, const WaitCtx& wc) {
+                              int blk0, int nb, int hidden, uint8_t* slots,
+                              uint32_t slot_bytes, uint64_t* full, uint64_t* empty, const WaitCtx& wc) {
   const int lane = threadIdx.x & 31, part = lane & 3;
   const int tok = 8 * NG * grp + (lane >> 2);       // of the first group; + 8 g
+  const int not_live = hidden + tok;
   const int R = p.D - p.r;
   const int64_t page_bytes = q8_page_bytes(p.r, R);
   const uint8_t* cache = static_cast<const uint8_t*>(p.cache_q8);
@@ -90,12 +91,12 @@ MLA_DEVICE void dequant_pages(const DecodeParams& p, int cg, int r0, int r1, int
   int32_t page = next.page(p);
   uint4 codes[NG][NB];
   uint2 scales[NG];
-  int live;                              // tokens of the context from `tok` on
+  int live;                              // tokens that some row sees from `tok` on
   auto fetch = [&]() {
     if (page < 0 || page >= p.num_pages) page = 0;       // the TMA producer reports it
     const uint8_t* src = cache + page * page_bytes;
-    // rows past the context are loaded too (they are part of the page) but not used
-    live = next.w.L - (next.t - next.w.s) * kDecodeTok - tok;
+    // rows past those are loaded too (they are part of the page) but not used
+    live = next.w.L - (next.t - next.w.s) * kDecodeTok - not_live;
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
 #pragma unroll
@@ -118,8 +119,7 @@ MLA_DEVICE void dequant_pages(const DecodeParams& p, int cg, int r0, int r1, int
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
       if (live <= 8 * g) {
-        // rows past the context may hold anything: they become zeros (0-weight x garbage must
-        // not reach O)
+        // they may hold anything: they become zeros (0-weight x garbage must not reach O)
         scales[g] = make_uint2(0, 0);
 #pragma unroll
         for (int k = 0; k < NB; ++k) codes[g][k] = make_uint4(0, 0, 0, 0);

@@ -216,6 +216,11 @@ struct DecodeParams {
   const uint16_t* q_ext;     // [B, q*H, D]
   int32_t rope_half;         // rotary columns per CTA of the pair (G*d_r/2)
 };
+// Whether the rows of every block of `rows` see the same tokens: all rows see all, or a block lies
+// within one query token. The conversion of 8-bit pages then zeroes what a block does not see.
+inline bool same_rows_seen(const DecodeParams& p, int rows) {
+  return !p.causal || p.q_len == 1 || p.num_heads % rows == 0;
+}
 size_t decode_smem_bytes(int ncol, int nblk, int slot_blocks, int nslot, int npt);
 cudaError_t launch_decode(const DecodeParams& p, int ncol, dim3 grid, size_t smem,
                           cudaStream_t stream);

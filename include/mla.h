@@ -210,6 +210,10 @@ size_t mla_decode_workspace_size(const mla_dims* dims, int32_t batch, int32_t q_
  * The cached pages of all sequences are cut into equal ranges, one per CTA, so ragged
  * lengths balance; a sequence cut between CTAs is merged with the log-sum-exp identity
  * by a second, small kernel launched right after.
+ * Infinities and NaN in a token's cache row do not reach the query rows that do not see the token.
+ * A NaN makes o_latent and lse NaN in every row that sees it, whatever the splits; so does an
+ * infinity, but where it makes the token's score -inf: that token has weight 0, and whether 0 times
+ * its infinite latents counts as 0 or as NaN is not specified.
  *
  *   q_ext       bf16 [B, q, H, D]   from mla_absorb_q
  *   cache       bf16 [num_pages, ps, D]
