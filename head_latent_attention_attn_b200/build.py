@@ -21,7 +21,7 @@ SOURCES = ["host_common.cu", "api.cu", "append.cu", "wgemm.cu", "decode.cu", "de
            "noalloc.cu", "kv_shared.cu", "oproj.cu", "down_kv.cu", "combine.cu", "cache_q8.cu",
            "prefill.cu"]
 HEADERS = ["ptx.cuh", "kernels.h", "host_common.h", "decode_sched.cuh", "append.cuh", "q8.cuh",
-           "dequant.cuh"]
+           "dequant.cuh", "hide.cuh"]
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",

@@ -1048,6 +1048,9 @@ mla_status mla_prefill_attn(const mla_dims* dims, const void* q, const void* k_n
     maps = map4(&p.tm_qr, static_cast<const uint16_t*>(q) + dn, dr, H, q_len, dq, H * dq) &&
            map4(&p.tm_kr, k_pe, dr, G, kv_len, dr, k_pe_token_stride);
   if (!maps) return MLA_ERR_CUDA;
+  p.v = static_cast<const uint16_t*>(v);
+  p.v_token = v_token_stride;
+  p.v_head = v_head_stride;
   p.seq_lens = seq_lens;
   p.q_lens = q_lens;
   p.o = static_cast<uint16_t*>(o);

@@ -640,7 +640,8 @@ __global__ void __launch_bounds__(kBlockThreads<Q8>, 1)
                   packed[ch * 4 + 0], packed[ch * 4 + 1], packed[ch * 4 + 2], packed[ch * 4 + 3]);
             }
           }
-          // a token that some row does not see, or past the context, where a page may hold anything
+          // a token that some row does not see (the rows that see it have their NaN by its score, taken
+          // above), or past the context, where a page may hold anything
           // (over the 8-bit cache what no row sees is zero from the conversion on). The code
           // alone costs there (4 rows of 16 heads over 16 x 64K tokens 147 us instead of 143, 2 of 28
           // heads over 64 x 4096 51 instead of 47), so that blocks of rows which see the same tokens

@@ -532,7 +532,7 @@ __global__ void __launch_bounds__(kThreads<Q8>, 1)
     } else if (kHide && warp == kHideWarp && has_work) {
       // ========================== tokens that some row does not see ========================
       // Once S of a tile has been computed, such a token's latent half loses what a weight of 0 must
-      // not meet (see hide_token); over the bf16 cache what lies past the context is zeroed here too.
+      // not meet (see hide_token; the rows that see it have their NaN by its score); over the bf16 cache what lies past the context is zeroed here too.
       // Only these tiles wait for this warp. The same code in the owners' loop costs every tile,
       // whether it runs or not (64 x 8192 tokens over the 8-bit cache 252 to 293 us instead of 239).
       // This warp's hand-overs still cost 11 % there (4 rows of 32 heads, 64 x 4096 tokens: 148 us

@@ -8,6 +8,7 @@
 // afterwards with the log-sum-exp identity.
 #pragma once
 
+#include "hide.cuh"
 #include "kernels.h"
 #include "ptx.cuh"
 
@@ -70,54 +71,6 @@ struct RowsSeen {
 MLA_DEVICE int piece_slot(int i, int s, int per, int col_groups, int cg) {
   const int i0 = s / per;
   return 2 * (i * col_groups + cg) + ((i == i0 && s != i0 * per) ? 1 : 0);
-}
-
-// Whether the bf16 pairs of a 16-byte chunk are all finite: 0 * x is 0 or, for an infinity or a NaN,
-// NaN, which the sums keep.
-MLA_DEVICE uint32_t times_zero(uint32_t x, uint32_t sum) {
-  uint32_t r;
-  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(x), "r"(0u), "r"(sum));
-  return r;
-}
-
-// The 64 bf16 numbers of a token in a block of a cache slot (128 bytes at `row`, shared memory), for a
-// block of query rows of which some (or, with `none`, all) do not see the token. Their weight is 0, and
-// 0 times an infinity or a NaN must not reach their O: such numbers become zeros (with `none` all do).
-// A row that sees the token has its NaN by its score, which was taken before.
-MLA_DEVICE void hide_token(uint8_t* row, bool none, int lane) {
-  // chunks in another order a lane: rows are 128 bytes apart, so that eight lanes at the same chunk
-  // would be in the same banks
-  auto at = [&](int i) { return reinterpret_cast<uint4*>(row + 16 * ((i + lane) & 7)); };
-  if (none) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) *at(i) = make_uint4(0, 0, 0, 0);
-    return;
-  }
-  uint32_t sum = 0;
-#pragma unroll
-  for (int i = 0; i < 8; i += 4) {
-    uint4 x[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) x[j] = *at(i + j);
-    uint32_t a = 0, b = 0;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      a = times_zero(x[j].y, times_zero(x[j].x, a));
-      b = times_zero(x[j].w, times_zero(x[j].z, b));
-    }
-    sum |= a | b;
-  }
-  if ((sum & 0x7FFF7FFFu) == 0) return;          // (zeros of either sign)
-#pragma unroll 1
-  for (int i = 0; i < 8; ++i) {
-    uint32_t* w = reinterpret_cast<uint32_t*>(at(i));
-#pragma unroll 1
-    for (int j = 0; j < 4; ++j) {
-      const uint32_t lo = (w[j] & 0x7F80u) == 0x7F80u ? 0xFFFF0000u : 0xFFFFFFFFu;
-      const uint32_t hi = (w[j] & 0x7F800000u) == 0x7F800000u ? 0xFFFFu : 0xFFFFFFFFu;
-      w[j] &= lo & hi;
-    }
-  }
 }
 
 // Tile range [r0, r1) of virtual CTA vc among vgrid, and the sequence holding tile r0.

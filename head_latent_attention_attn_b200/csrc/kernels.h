@@ -243,6 +243,8 @@ struct PrefillParams {
   CUtensorMap tm_k;          // 4D {d_n, H, kv_len, B}
   CUtensorMap tm_kr;         // 4D {d_r, G, kv_len, B}
   CUtensorMap tm_v;          // 4D {d_v, H, kv_len, B}
+  const uint16_t* v;         // token t of sequence b, head h at (b kv_len + t) v_token + h v_head
+  int64_t v_token, v_head;
   const int32_t* seq_lens;   // [B]
   const int32_t* q_lens;     // [B] or null: all q_len
   uint16_t* o;               // [B, q_len, H, d_v]

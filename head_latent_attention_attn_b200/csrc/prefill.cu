@@ -45,6 +45,7 @@
 // more than 8 (weights stay <= 256), so that O is rescaled rarely; the row itself then does it.
 #include <math.h>
 
+#include "hide.cuh"
 #include "kernels.h"
 #include "ptx.cuh"
 
@@ -75,7 +76,8 @@ constexpr uint32_t kMiscOff = kRopeOff + 2 * kBlk;
 constexpr uint32_t kBars = 4 + 2 * kSlots + 10 + 6;
 constexpr uint32_t kInfoOff = kMiscOff + 16;     // [2] unit descriptions, 32 bytes each
 constexpr uint32_t kRespOff = kInfoOff + 64;     // answer of the launch control, 16 bytes
-constexpr uint32_t kBarOff = kRespOff + 16;
+constexpr uint32_t kBadOff = kRespOff + 16;      // [4] see mark_bad
+constexpr uint32_t kBarOff = kBadOff + 16;
 constexpr uint32_t kSmem = kBarOff + 8 * kBars + 1024;   // + alignment slack
 static_assert(kSmem <= 232448, "shared memory of a CTA");
 
@@ -84,6 +86,10 @@ static_assert(kSmem <= 232448, "shared memory of a CTA");
 struct Unit {
   int row0, h, b, L, ql, nt[2], t0;
   MLA_DEVICE int tiles() const { return max(nt[0], nt[1]); }
+  // first position that some row of the unit does not see
+  MLA_DEVICE int first_hidden(const PrefillParams& p) const {
+    return p.causal ? min(L, L - ql + row0 + 1) : L;
+  }
 };
 
 // Unit u of the grid, or with split > 1 the part of its tiles that CTA `rank` of the cluster takes.
@@ -191,6 +197,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&empty[i], 1);
     }
     *abort_flag = 0;
+    for (int i = 0; i < 4; ++i) reinterpret_cast<uint32_t*>(base + kBadOff)[i] = 0;
     fence_mbar_init();
   }
   if (warp == 1) {
@@ -469,12 +476,39 @@ __global__ void __launch_bounds__(kThreads, 1)
     Unit w, staged;                              // kSplit: the unit whose part is in O
     staged.h = -1;
     float m_part = kRefInit, l_part = 0.0f;
+    bool bad_part = false;
+    // The k-th unit has values among those that some row does not see which are infinite or NaN. The
+    // stamp of a unit four before may go: no group is three units behind the other.
+    volatile uint32_t* bad_unit = reinterpret_cast<uint32_t*>(base + kBadOff);
+    // Those values, taken out of the tiles, for the rows that see them: column e + i of this thread's
+    // row in o[i].
+    auto add_hidden = [&](const Unit& u, int ng, float* o, int e) {
+      const int qi = u.row0 + g * kRows + 32 * sp + lane;
+      const int last = min(min(u.L - 1, u.L - u.ql + qi), (u.t0 + ng) * kTok - 1);
+#pragma unroll 1
+      for (int t = max(u.first_hidden(p), u.t0 * kTok); t <= last; ++t) {
+        const uint16_t* v = p.v + (int64_t(u.b) * p.kv_len + t) * p.v_token + u.h * p.v_head + e;
+#pragma unroll
+        for (int i = 0; i < 32; i += 8) {
+          if (e + i >= p.dv) break;
+          const uint4 x = *reinterpret_cast<const uint4*>(v + i);
+          const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            if ((w[j] & 0x7F80u) == 0x7F80u) o[i + 2 * j] += __uint_as_float(w[j] << 16);
+            if ((w[j] & 0x7F800000u) == 0x7F800000u)
+              o[i + 2 * j + 1] += __uint_as_float(w[j] & 0xFFFF0000u);
+          }
+        }
+      }
+    };
     for (uint32_t k = 0; ok && next_unit(k, &w, true); ++k) {
       const int n = w.tiles(), ng = g == 0 ? w.nt[0] : w.nt[1];
       const int L = w.L, ql = w.ql;
       const int qi = w.row0 + g * kRows + 32 * sp + lane;     // query row of this thread
       // last token that this row sees (may be negative)
       const int lim = min(L - 1, p.causal ? L - ql + qi : L - 1);
+      const int hidden = w.first_hidden(p);
       float m = kRefInit, l = 0.0f;
       for (int j = 0; j < n; ++j) {
         v_ring.next();                           // V of tile j
@@ -483,14 +517,35 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (j >= ng) continue;
         const uint32_t parity = tiles & 1;
         ++tiles;
-        ok = __all_sync(0xffffffffu, mbar_wait(&s_full[g], parity, wc));
+        const int t0 = (w.t0 + j) * kTok;
+        // Value rows past the context may hold anything, and a weight of 0 times NaN is NaN: zeros. Of a
+        // token that some row of the unit does not see, infinities and NaN become zeros, and the rows
+        // that see it add them at the end. Group 0 does this for its tiles, which the product of group
+        // 1 meets after group 0's, and group 1 for those that only it has. Where there is a tile
+        // before, that is done by the time the scores come (for every tile after them: 2 x 4096 causal
+        // rows 344 us, 331 without any). Its scores also say that the slot's last keys had landed, so
+        // that the phase waited for is this tile's; with the unit's first tile its own scores do.
+        const bool hides = t0 + kTok > hidden && (g == 0 || j >= w.nt[0]);
+        auto hide = [&]() {
+          ok = __all_sync(0xffffffffu, mbar_wait(&full[at.slot], at.round & 1, wc));
+          const int tok = 32 * sp + lane;
+          if (ok && t0 + tok >= hidden) {
+            uint8_t* v = base + kSlotOff + at.slot * 2 * kBlk + tok * 128;
+            bool bad = false;
+            for (int e = 0; e < vb; ++e) bad |= hide_token(v + e * kBlk, t0 + tok >= L, lane);
+            if (bad) bad_unit[k & 3] = k + 1;
+          }
+          fence_proxy_async_smem();
+        };
+        if (hides && j > 0) hide();
+        ok = ok && __all_sync(0xffffffffu, mbar_wait(&s_full[g], parity, wc));
+        if (ok && hides && j == 0) hide();
         if (!ok) break;
         tc_fence_after();
         float s[kTok];
 #pragma unroll
         for (int e = 0; e < kTok; e += 32) tmem_ld32(t_s + e, s + e);
         tmem_wait_ld();
-        const int t0 = (w.t0 + j) * kTok;
         if (t0 + kTok - 1 > lim) {
 #pragma unroll
           for (int e = 0; e < kTok; ++e)
@@ -526,21 +581,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = 0; i < 16; ++i) o[i] *= alpha;
             tmem_st16(t_o + e, o);
           }
-        }
-        if (t0 + kTok > L) {
-          // value rows past the context may hold anything (0-weight x NaN is NaN): zero them.
-          // Both groups do so; the second writes zeros over zeros.
-          ok = __all_sync(0xffffffffu, mbar_wait(&full[at.slot], at.round & 1, wc));
-          if (!ok) break;
-          const int tok = 32 * sp + lane;
-          if (t0 + tok >= L) {
-            uint8_t* v = base + kSlotOff + at.slot * 2 * kBlk + tok * 128;
-            for (int e = 0; e < vb; ++e)
-#pragma unroll
-              for (int i = 0; i < 8; ++i)
-                *reinterpret_cast<uint4*>(v + e * kBlk + 16 * i) = make_uint4(0, 0, 0, 0);
-          }
-          fence_proxy_async_smem();
         }
         // weights 2^(s * scale - m), in pairs, half a tile at a time
         const float2 c2 = make_float2(c, c), m2 = make_float2(-m, -m);
@@ -578,9 +618,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         staged = w;
         m_part = m;
         l_part = l;
+        bad_part = ng > 0 && bad_unit[k & 3] == k + 1;
         break;
       }
-      const bool real = qi < ql;
+      const bool real = qi < ql, bad = ng > 0 && bad_unit[k & 3] == k + 1;
       const int64_t row = (int64_t(w.b) * p.q_len + qi) * p.heads + w.h;
       const float inv = l != 0.0f ? 1.0f / l : 0.0f;          // NaN stays NaN
       if (real) p.lse[row] = l != 0.0f ? (m + __log2f(l)) * kLn2 : -INFINITY;
@@ -592,6 +633,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_ld32(t_o + e, o);
           tmem_wait_ld();
         }
+        if (bad) add_hidden(w, ng, o, e);
 #pragma unroll
         for (int i = 0; i < 32; i += 8) {
           uint32_t x[4];
@@ -625,6 +667,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_ld32(t_o + e, o);
             tmem_wait_ld();
           }
+          if (bad_part) add_hidden(staged, g == 0 ? staged.nt[0] : staged.nt[1], o, e);
 #pragma unroll
           for (int i = 0; i < 32; i += 4)
             *stage_o(base, g, (e + i) / 4, at) =

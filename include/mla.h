@@ -317,9 +317,10 @@ mla_status mla_decode_attn_q8(const mla_dims* dims, const void* q_ext, const voi
  *   dev_error int32 device error word or NULL
  * Row i sees token t < L, and with causal != 0 only t <= L - q_lens[b] + i; a row that sees none
  * (L < q_lens[b], or L = 0) gives o = 0 and lse = -inf. What lies past L in k_nope, k_pe and v is
- * not used. A NaN or infinity in the value of a token t < L makes o NaN also for the rows of its
- * 128-row block that do not see t. A length out of range sets MLA_DEVERR_BOUNDS; that sequence
- * then sees nothing. P is rounded to bf16 as a tensor-core operand; scores, sums and o are fp32.
+ * not used, and infinities and NaN in a token's key or value do not reach the rows that do not see
+ * it; the rows that see them have them in o by the formula. A length out of range sets
+ * MLA_DEVERR_BOUNDS; that sequence then sees nothing. P is rounded to bf16 as a tensor-core operand;
+ * scores, sums and o are fp32.
  * Needs no workspace; q and kv_len are at least 1. Requires d_n <= 128, d_v <= 128, d_r <= 64 and a
  * multiple of 8 (MLA_ERR_UNSUPPORTED otherwise).
  */

@@ -6,6 +6,7 @@ import torch
 
 import head_latent_attention_attn_b200 as mla
 from tests import q8_reference as Q
+from tests.test_gpu_prefill_expanded import check, make, run
 from tests.test_gpu_q8 import SHAPES, Filled, bf, bits_of, bounds_of, cu, decode
 
 pytestmark = pytest.mark.gpu
@@ -119,3 +120,120 @@ def test_a_bad_block_does_not_reach_rows_that_do_not_see_it(name, q, lens, ns):
     for b, L in enumerate(lens):
         sees = torch.arange(L - q, L) >= bad.get(b, L)
         assert bool(torch.isfinite(o[b, ~sees].float()).all()) and bool(torch.isfinite(lse[b, ~sees]).all())
+
+
+def number(bits):
+    return float(Q.bf16_to_f64(np.array([bits], np.uint16))[0])
+
+
+# heads, groups, d_n, d_r, d_v; query rows, keys, lengths, query lengths
+PREFILL = {
+    "clusters": (4, 1, 128, 64, 128, 77, 1100, [1100, 333, 77], [77, 70, 77]),
+    "two_row_tiles": (2, 1, 64, 0, 64, 300, 700, [700, 301, 513], [300, 300, 130]),
+    "odd": (3, 3, 96, 24, 72, 260, 260, [260, 200, 131], [260, 199, 131]),
+    "short_of_rows": (2, 2, 40, 64, 128, 200, 150, [150, 3, 0], [200, 200, 200]),
+    "many_units": (96, 1, 64, 16, 64, 300, 700, [700, 650, 257], [300, 257, 257]),
+    "one_token": (4, 1, 16, 8, 16, 1, 130, [130, 1, 128], [1, 1, 1]),
+}
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("name", sorted(PREFILL))
+def test_prefill_values_reach_only_rows_that_see_them(name, causal):
+    """Infinities and NaN among the values of single tokens, at the chunk's borders and inside it: a row
+    that sees one has it in that column, on top of what it has without (and NaN where both signs
+    meet); every other number keeps its bits."""
+    H, G, dn, dr, dv, q, n, lens, q_lens = PREFILL[name]
+    d = mla.make_dims(H, G, 64, dn, dr, dv, 64, 1.0 / np.sqrt(dn + dr))
+    x = make(len(lens), q, n, H, G, dn, dr, dv, seed=q)
+    rng = np.random.default_rng(n)
+    marks = []                                   # (sequence, token, head, column, bits)
+    for b, (L, m) in enumerate(zip(lens, q_lens)):
+        at = {L - 1, L - 2, L - m, L - m + 1, L - m + 63, L - m + 127, L - m + 128, L - m + 129,
+              L - m + 255, L - m + 256, 0, L // 2}
+        at |= {int(t) for t in rng.integers(max(L - m, 0), max(L, 1), 4)}
+        marks += [(b, t, int(rng.integers(H)), int(rng.integers(dv)), bits)
+                  for t in sorted(at) if 0 <= t < L for bits in (NAN, INF, NINF)]
+    y = {k: v.copy() for k, v in x.items()}
+    for b, t, h, c, bits in marks:
+        x["v"][b, t, h, c] = 0
+        y["v"][b, t, h, c] = bits
+    o0, lse0, st0 = run(d, x, lens, q_lens, causal, packed=dr > 0)
+    o, lse, st = run(d, y, lens, q_lens, causal, packed=dr > 0)
+    assert st == st0 == mla.MLA_OK
+    want, got = Q.bf16_to_f64(bits_of(o0)), Q.bf16_to_f64(bits_of(o))
+    for b, t, h, c, bits in marks:
+        L, m = lens[b], q_lens[b]
+        last = L - m + np.arange(m) if causal else np.full(m, L - 1)
+        with np.errstate(invalid="ignore"):
+            want[b, :m, h, c] += np.where(last >= t, number(bits), 0.0)
+    assert torch.equal(lse, lse0)
+    bad = np.argwhere(~((got == want) | (np.isnan(got) & np.isnan(want))))
+    assert bad.size == 0, f"{len(bad)} numbers differ, first {bad[:4].tolist()}"
+
+
+@pytest.mark.parametrize("name", sorted(PREFILL))
+def test_prefill_keys_reach_only_rows_that_see_them(name):
+    """A NaN in a key, and one in a group's rotary key: o and lse are NaN in the rows that see it, and
+    the others keep their bits."""
+    H, G, dn, dr, dv, q, n, lens, q_lens = PREFILL[name]
+    d = mla.make_dims(H, G, 64, dn, dr, dv, 64, 1.0 / np.sqrt(dn + dr))
+    x = make(len(lens), q, n, H, G, dn, dr, dv, seed=q)
+    o0, lse0, _ = run(d, x, lens, q_lens)
+    y = {k: v.copy() for k, v in x.items()}
+    sees = np.zeros((len(lens), q, H), bool)
+    for b, (L, m) in enumerate(zip(lens, q_lens)):
+        pos = L - m + np.arange(m)
+        for t in {L - 1, L - (m + 1) // 2}:
+            if 0 <= t < L:
+                h = (t + b) % H
+                y["k"][b, t, h, dn - 1] = NAN
+                sees[b, :m, h] |= pos >= t
+                if dr and t == L - 1:
+                    g = (h + 1) % H // (H // G)
+                    y["kr"][b, t, g, 0] = NAN
+                    sees[b, :m, g * (H // G):(g + 1) * (H // G)] |= (pos >= t)[:, None]
+    o, lse, st = run(d, y, lens, q_lens)
+    assert st == mla.MLA_OK
+    s = torch.from_numpy(sees).cuda()
+    assert bool(torch.isnan(lse[s]).all()) and bool(torch.isnan(o[s].float()).all())
+    assert torch.equal(lse[~s], lse0[~s]) and torch.equal(o[~s], o0[~s])
+
+
+def test_prefill_units_after_one_with_bad_values():
+    """A CTA that takes over units, and a unit with nothing bad right after one that has it: only the
+    heads with bad values differ, over and over."""
+    H, G, dn, dr, dv, q, n, lens, q_lens = PREFILL["many_units"]
+    d = mla.make_dims(H, G, 64, dn, dr, dv, 64, 1.0 / np.sqrt(dn + dr))
+    x = make(len(lens), q, n, H, G, dn, dr, dv, seed=5)
+    o0, lse0, _ = run(d, x, lens, q_lens)
+    y = {k: v.copy() for k, v in x.items()}
+    heads = np.arange(0, H, 3)
+    for b, L in enumerate(lens):
+        y["v"][b, L - 1, heads] = NAN            # seen by the last row only
+    for _ in range(5):
+        o, lse, _ = run(d, y, lens, q_lens)
+        assert torch.equal(lse, lse0)
+        for b, m in enumerate(q_lens):
+            assert bool(torch.isnan(o[b, m - 1, heads].float()).all())
+            o[b, m - 1, heads] = o0[b, m - 1, heads]
+        assert torch.equal(o, o0)
+
+
+def test_prefill_of_many_short_prompts_with_garbage_behind_them():
+    """Hundreds of units of one to three tiles, whose last tile ends inside or behind its context: the
+    CTAs take over unit after unit while the tiles of the one before are still on their way."""
+    H, G, dn, dr, dv, B, q = 96, 1, 64, 16, 64, 12, 300
+    d = mla.make_dims(H, G, 64, dn, dr, dv, 64, 1.0 / np.sqrt(dn + dr))
+    x = make(B, q, q, H, G, dn, dr, dv, seed=9)
+    lens = [300, 1, 130, 128, 77, 256, 200, 257, 5, 129, 64, 260]
+    for b, L in enumerate(lens):
+        for k in ("k", "kr", "v"):
+            x[k][b, L:] = NAN
+        x["q"][b, L:] = NAN
+    o0, lse0, st = run(d, x, lens, lens)
+    assert st == mla.MLA_OK
+    check(d, x, lens, lens, True, o0, lse0, [0, 47, 95])
+    for _ in range(20):
+        o, lse, _ = run(d, x, lens, lens)
+        assert torch.equal(o, o0) and torch.equal(lse, lse0)
