@@ -726,6 +726,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       cluster_sync_all();
     }
+    __syncwarp();                                // (the merge's rows; a warp comes as one)
     cluster_sync_all();                          // nobody leaves while its part may be read
   }
   tc_fence_before();
