@@ -1014,6 +1014,7 @@ mla_status mla_prefill_attn(const mla_dims* dims, const void* q, const void* k_n
   if (batch < 0 || q_len <= 0 || kv_len <= 0 || (causal != 0 && causal != 1))
     return MLA_ERR_INVALID_ARG;
   if (dn > 128 || dv > 128 || dr > 64 || dr % 8 != 0) return MLA_ERR_UNSUPPORTED;
+  if (q_len > kPrefillMaxLen || kv_len > kPrefillMaxLen) return MLA_ERR_UNSUPPORTED;
   if (batch == 0) return MLA_OK;
   if (!q || !k_nope || !v || !seq_lens || !o || !lse || (dr > 0 && !k_pe))
     return MLA_ERR_INVALID_ARG;
@@ -1023,14 +1024,17 @@ mla_status mla_prefill_attn(const mla_dims* dims, const void* q, const void* k_n
   // a head's row lies inside its stride, and the heads of a token inside the token's; TMA
   // strides are multiples of 16 bytes below 2^40
   auto strides_ok = [&](int64_t tok, int64_t head, int width, int heads) {
-    return head >= width && tok >= head * (heads - 1) + width && head % 8 == 0 && tok % 8 == 0 &&
-           tok < (int64_t(1) << 38) / kv_len;
+    return head >= width && tok >= width && (tok - width) / head >= heads - 1 && head % 8 == 0 &&
+           tok % 8 == 0 && tok < (int64_t(1) << 38) / kv_len;
   };
   if (!strides_ok(k_token_stride, k_head_stride, dn, H) ||
       !strides_ok(v_token_stride, v_head_stride, dv, H) ||
       (dr > 0 && !strides_ok(k_pe_token_stride, dr, dr, G)))
     return MLA_ERR_INVALID_ARG;
-  if (int64_t(H) * batch * ((int64_t(q_len) + 255) / 256) > INT32_MAX) return MLA_ERR_UNSUPPORTED;
+  const int64_t heads_all = int64_t(H) * batch;
+  if (heads_all > INT32_MAX) return MLA_ERR_UNSUPPORTED;
+  const int64_t units = heads_all * ((q_len + 255) / 256);
+  if (units > INT32_MAX) return MLA_ERR_UNSUPPORTED;
   PrefillParams p{};
   const int64_t dq = dn + dr;
   auto map4 = [&](CUtensorMap* m, const void* at, int width, int heads, int64_t len,
@@ -1068,11 +1072,10 @@ mla_status mla_prefill_attn(const mla_dims* dims, const void* q, const void* k_n
   // half of the 126 MB L2 for the keys and values of the heads in work
   const int64_t head_bytes = int64_t(kv_len) * (dn + dv) * 2;
   p.head_block = int32_t(std::max<int64_t>(
-      1, std::min<int64_t>(int64_t(H) * batch, (int64_t(64) << 20) / head_bytes)));
+      1, std::min<int64_t>(heads_all, (int64_t(64) << 20) / head_bytes)));
   // Clusters of CTAs share the tiles of a unit, as large as they can be while they all fit on the
   // device at once and each CTA is left at least two tiles: 16 units of 36 tiles take 72 us with one
   // CTA each, 42 with two, 26 with four, 22.6 with six and 38.6 with eight, of which 15 clusters fit.
-  const int64_t units = int64_t(H) * batch * ((int64_t(q_len) + 255) / 256);
   const int tiles = (kv_len + 127) / 128;
   p.split = std::min(kPrefillMaxSplit, std::max(1, tiles / 2));
   while (p.split > 1 && (units * p.split > num_sms() || units > prefill_max_clusters(p.split)))

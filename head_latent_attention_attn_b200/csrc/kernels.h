@@ -255,6 +255,9 @@ struct PrefillParams {
   int32_t split;             // CTAs (a cluster) that share the tiles of 256 query rows: 1, 2, 4, 8
   float scale_log2;          // softmax_scale * log2(e)
 };
+// Query rows and tokens a call takes at most: tile arithmetic in 32 bits, and a unit of that many tokens
+// (262,144 tiles of some 2.2 us, 0.6 s) well within the 2 s that its scheduler warp waits for its end.
+constexpr int kPrefillMaxLen = 1 << 25;
 // Clusters of `split` CTAs of the kernel that are resident at once on the current device (0 on an
 // error), remembered: a cluster's CTAs share a GPC, so that not every SM can be in one.
 constexpr int kPrefillMaxSplit = 8;

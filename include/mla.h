@@ -321,8 +321,8 @@ mla_status mla_decode_attn_q8(const mla_dims* dims, const void* q_ext, const voi
  * it; the rows that see them have them in o by the formula. A length out of range sets
  * MLA_DEVERR_BOUNDS; that sequence then sees nothing. P is rounded to bf16 as a tensor-core operand;
  * scores, sums and o are fp32.
- * Needs no workspace; q and kv_len are at least 1. Requires d_n <= 128, d_v <= 128, d_r <= 64 and a
- * multiple of 8 (MLA_ERR_UNSUPPORTED otherwise).
+ * Needs no workspace; q and kv_len are at least 1 and at most 2^25 (MLA_ERR_UNSUPPORTED beyond).
+ * Requires d_n <= 128, d_v <= 128, d_r <= 64 and a multiple of 8 (MLA_ERR_UNSUPPORTED otherwise).
  */
 mla_status mla_prefill_attn(const mla_dims* dims, const void* q, const void* k_nope,
                             int64_t k_token_stride, int64_t k_head_stride, const void* k_pe,

@@ -1,0 +1,26 @@
+"""Sizes and strides at the ends of their types, without a GPU: refused or planned for, never wrapped."""
+import pytest
+
+import head_latent_attention_attn_b200 as mla
+from tests.test_abi_host import _dims
+from tests.test_abi_prefill import _prefill
+
+BIG = (1 << 31) - 1
+
+
+def test_prefill_sizes(mla_lib):
+    """Row and token counts that 32-bit tile arithmetic would wrap on, or whose units take longer than
+    a wait in the kernel may."""
+    d = _dims(num_heads=1, qk_nope_dim=8, v_head_dim=8, rope_dim=0)
+    small = dict(kts=8, khs=8, vts=8, vhs=8, kr=None, krts=0, batch=1)
+    for kw in (dict(qlen=BIG), dict(kvlen=BIG), dict(qlen=(1 << 25) + 1), dict(kvlen=(1 << 25) + 1)):
+        assert _prefill(d, **{**small, **kw}) == mla.MLA_ERR_UNSUPPORTED
+    many = _dims(num_heads=1 << 30, num_kv_groups=1)
+    wide = dict(kts=1 << 37, khs=128, vts=1 << 37, vhs=128, kvlen=1)
+    assert _prefill(many, batch=1 << 30, qlen=1 << 12, **wide) == mla.MLA_ERR_UNSUPPORTED
+
+
+@pytest.mark.parametrize("which", ["k", "v"])
+@pytest.mark.parametrize("stride", [1 << 61, (1 << 62) + 8, 1 << 58])
+def test_prefill_head_strides(mla_lib, which, stride):
+    assert _prefill(_dims(), **{which + "hs": stride}) == mla.MLA_ERR_INVALID_ARG
