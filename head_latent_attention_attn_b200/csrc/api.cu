@@ -700,7 +700,7 @@ struct RowsPlan {
 
 RowsPlan plan_rows(const mla_dims* d, const DecodePlan& P, int32_t batch, int32_t max_seq_len) {
   RowsPlan C{};
-  C.tiles = (max_seq_len + kDecodeTok - 1) / kDecodeTok;
+  C.tiles = int32_t((int64_t(max_seq_len) + kDecodeTok - 1) / kDecodeTok);
   const int64_t tokens = int64_t(batch) * C.tiles * kDecodeTok;
   if (P.col_groups < 3 || batch == 0 || tokens > (int64_t(1) << 31) - kDecodeTok) return C;
   // a plan with one range per block of query rows cuts no sequence: its partials go unused

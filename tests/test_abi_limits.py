@@ -24,3 +24,14 @@ def test_prefill_sizes(mla_lib):
 @pytest.mark.parametrize("stride", [1 << 61, (1 << 62) + 8, 1 << 58])
 def test_prefill_head_strides(mla_lib, which, stride):
     assert _prefill(_dims(), **{which + "hs": stride}) == mla.MLA_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("q", [3, 256])
+def test_workspace_of_a_context_without_a_bound(mla_lib, q):
+    """The larger workspace of a context that it cannot hold is the plain one."""
+    d = _dims()
+    for n in (BIG, BIG - 62):
+        plain = mla.mla_decode_workspace_size(d, 1, q, n)
+        assert plain > 0 and mla.mla_decode_q8_workspace_size(d, 1, q, n) == plain
+    n = 1 << 20
+    assert mla.mla_decode_q8_workspace_size(d, 1, q, n) > mla.mla_decode_workspace_size(d, 1, q, n)
