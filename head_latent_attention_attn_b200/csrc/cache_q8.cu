@@ -126,7 +126,7 @@ __global__ void __launch_bounds__(256) cache_append_q8_kernel(AppendQ8Params p) 
   uint8_t* dst = p.cache + page * q8_page_bytes(p.r, R);
 
   uint8_t* codes = dst + slot * kQ8Cols + 16 * part;
-  uint64_t scales = 0;                         // byte k: block k, of the blocks of this lane
+  uint64_t scales = 0;                         // byte k: block k, of this lane's; 0 past r / 64
 #pragma unroll
   for (int i = 0; i < TOK; ++i) {
     const int k = blk0 + i * kStep;
@@ -156,7 +156,7 @@ __global__ void __launch_bounds__(256) cache_append_q8_kernel(AppendQ8Params p) 
     if (mine && k < nb)
       *reinterpret_cast<uint4*>(codes + k * kQ8BlockBytes) =
           make_uint4(code[0], code[1], code[2], code[3]);
-    scales |= uint64_t(s) << (8 * k);
+    scales |= uint64_t(k < nb ? s : 0u) << (8 * k);
   }
 #pragma unroll
   for (int o = 4 * TOK; o < 32; o <<= 1) scales |= __shfl_xor_sync(0xffffffffu, scales, o);

@@ -3,7 +3,7 @@
 // A page holds 64 tokens. Its bytes are three planes, in this order:
 //   codes   [r/64][64 tokens][64]   e4m3 code of latent column 64 k + j of token t
 //   keys    [64 tokens][R]          rotated keys of every group, bf16 (R = G * d_r)
-//   scales  [64 tokens][8]          byte k: exponent + 127 of the token's column block k
+//   scales  [64 tokens][8]          byte k: exponent + 127 of the token's column block k; 0 past r/64
 // The codes are blocked by 64 columns so that 8 tokens of a block are 512 consecutive bytes
 // (one 16-byte load a lane) and a thread's 16 codes become two 16-byte chunks of the
 // 128-byte-swizzled bf16 operand tile without a shared-memory bank conflict.

@@ -240,7 +240,7 @@ mla_status mla_decode_attn(const mla_dims* dims, const void* q_ext, const void* 
  * A cache page is mla_q8_page_bytes(dims) = 64 (r + 2 R + 8) bytes, R = G*d_r, for 64 tokens:
  *   codes   [r/64][64 tokens][64]  e4m3 code of latent column 64 k + j of token t
  *   keys    [64 tokens][R]         bf16, rotated keys of every group
- *   scales  [64 tokens][8]         byte k: exponent + 127 of the token's column block k
+ *   scales  [64 tokens][8]         byte k: exponent + 127 of the token's column block k; 0 past r/64
  * Block k of token t holds x = code * 2^(byte - 127), which is exact in bf16. The exponent is the
  * least e in [-110, 119] with max|x| * 2^-e <= 448 over the block's 64 columns; the codes are
  * round-to-nearest-even of x * 2^-e (beyond 448 * 2^119 they saturate). A block that holds an
