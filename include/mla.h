@@ -299,8 +299,11 @@ mla_status mla_decode_attn_q8(const mla_dims* dims, const void* q_ext, const voi
  * page): a key and a value per head, the rotary key shared by the heads of a group. For a chunk
  * of many new tokens this is the cheaper form: d_n + d_r + d_v multiplications a (query, token)
  * pair and head instead of the absorbed form's 2 r + d_r. The keys and values of a context are
- * expanded from its latents once a chunk (mla_out_up with W_UK, and with W_UV, on the rows that
- * mla_cache_read_q8 returns or on the new tokens' c_kv).
+ * expanded from its latents once a chunk: mla_out_up with W_UK and dims whose v_head_dim is d_n gives
+ * k_nope, with W_UV it gives v. Its o_latent is then [B*kv_len, H, r], a token's latent once for every
+ * head, which the caller copies there: mla_out_up reads rows*H*r numbers, so that neither the rows
+ * [B, n, D] of mla_cache_read_q8 nor c_kv [B, n, r] may be passed as they are. The rotary part of the
+ * query is rotated as mla_absorb_q leaves it in q_ext, in columns r + g(h)*d_r on.
  *
  *   q         bf16 [B, q, H, d_n + d_r]   query, its rotary part rotated
  *   k_nope    bf16, token t of sequence b and head h at ((b*kv_len + t)*k_token_stride +
