@@ -4,7 +4,7 @@ import pytest
 
 import head_latent_attention_attn_b200 as mla
 from tests import q8_reference as Q
-from tests.test_gpu_q8 import SHAPES, bf, cu, dims_of, to_bits
+from tests.test_gpu_q8 import SHAPES, Filled, bf, check_attention, cu, decode, dims_of, to_bits
 
 pytestmark = pytest.mark.gpu
 
@@ -37,3 +37,22 @@ def test_pages_do_not_depend_on_the_call(name):
                                     cu(sin[:, a:b]), cu(table), cu(np.array([start + a], np.int32)), cache)
         bad = np.argwhere(cache.cpu().numpy() != want)
         assert bad.size == 0, f"cuts {cuts}: {len(bad)} bytes differ, first {bad[:4].tolist()}"
+
+
+@pytest.mark.parametrize("name", ["deepseek_v2", "qwen3_30b_a3b", "rank_192"])
+@pytest.mark.parametrize("power", [-100, -60, 14, 100])
+def test_attention_over_any_scale(name, power):
+    """Latents of about 2^power and queries of about 2^-power, without keys: scores of order one that
+    come from the scaled codes alone, so that o, lse and the softmax tell a wrong scale."""
+    f = Filled(name, [150, 64], seed=4, size=2.0 ** power)
+    B = len(f.lens)
+    f.k_bits[...] = 0
+    mla.mla_cache_append_q8(f.dims, bf(f.c_bits), bf(f.k_bits), cu(f.cos), cu(f.sin), cu(f.table),
+                            cu(np.zeros(B, np.int32)), f.cache, new_lens=cu(np.array(f.lens, np.int32)),
+                            dev_error=f.err)
+    q_bits = to_bits(Q.bf16_to_f64(f.query(1)) * 2.0 ** -power)
+    o, lse = decode(f.dims, mla.mla_decode_attn_q8, q_bits, f.cache, f.table, f.lens)
+    check_attention(o, lse, q_bits, f)
+    spread = lse.max() - lse.min()
+    assert float(spread) > 1e-3, "scores that say nothing"
+    assert mla.mla_get_device_status(f.err) == mla.MLA_OK
