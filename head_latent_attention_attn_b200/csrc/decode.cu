@@ -222,9 +222,9 @@ size_t decode_smem_bytes(int ncol, int nblk, int slot_blocks, int nslot, int npt
   return decode_layout(ncol, nblk, slot_blocks, nslot, npt).total;
 }
 
-// kHide: some rows of a block may not see a token that others see, or (bf16 cache) a page may hold
-// more than the context.
-template <int NCOL, bool Q8, bool kHide>
+// kSee: what the rows of a block see. Over the bf16 cache, where a page may also hold more than the
+// context, it is always kSeeSome.
+template <int NCOL, bool Q8, RowsSee kSee>
 __global__ void __launch_bounds__(kBlockThreads<Q8>, 1)
     mla_decode_kernel(const __grid_constant__ DecodeParams p) {
   constexpr int HALF = NCOL / 2;
@@ -464,7 +464,7 @@ __global__ void __launch_bounds__(kBlockThreads<Q8>, 1)
     if constexpr (Q8) reg_dec<kRegsDequant>();
     if (has_work) {
       const int wi = warp - kDqWarp0, lb = p.r / kQ8Cols;
-      const int hidden = RowsSeen(p, cg, NCOL).hidden_all;
+      const int hidden = kSee == kSeeAll ? 0 : RowsSeen(p, cg, NCOL).hidden_all;
       if (dequant_warps<NCOL>(p.r) == 4) {
         if (wi < 4)
           dequant_pages<4, 2>(p, cg, r0, r1, sched[0], sched[1], wi, 0, lb, hidden, slots, slot_bytes,
@@ -645,8 +645,8 @@ __global__ void __launch_bounds__(kBlockThreads<Q8>, 1)
           // (over the 8-bit cache what no row sees is zero from the conversion on). The code
           // alone costs there (4 rows of 16 heads over 16 x 64K tokens 147 us instead of 143, 2 of 28
           // heads over 64 x 4096 51 instead of 47), so that blocks of rows which see the same tokens
-          // have an instance without it (kHide).
-          if (kHide && ragged && pos >= L - seen_by.hidden_some && !(Q8 && pos >= L - seen_by.hidden_all)) {
+          // have instances without it (RowsSee).
+          if (kSee == kSeeSome && ragged && pos >= L - seen_by.hidden_some && !(Q8 && pos >= L - seen_by.hidden_all)) {
             (void)mbar_try_wait(&full[slot], ring.round & 1);   // long complete: the page's bytes
             uint8_t* row = slots + slot * slot_bytes + tok * 128;
             for (int k = hf; k < (p.r + 63) / 64; k += 2)
@@ -737,27 +737,30 @@ extern "C" int mla_trace_read(unsigned long long* host, int n) {
 #endif
 
 
-template <int NCOL, bool Q8, bool kHide>
+template <int NCOL, bool Q8, RowsSee kSee>
 static cudaError_t launch_decode_n(const DecodeParams& p, dim3 grid, size_t smem,
                                    cudaStream_t stream) {
   if (Q8) {
     static std::atomic<bool> known{false};
-    const cudaError_t e = check_launch_regs(mla_decode_kernel<NCOL, Q8, kHide>, kRegsLaunch, &known);
+    const cudaError_t e = check_launch_regs(mla_decode_kernel<NCOL, Q8, kSee>, kRegsLaunch, &known);
     if (e != cudaSuccess) return e;
   }
-  cudaError_t e = cudaFuncSetAttribute(mla_decode_kernel<NCOL, Q8, kHide>,
+  cudaError_t e = cudaFuncSetAttribute(mla_decode_kernel<NCOL, Q8, kSee>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
   if (e != cudaSuccess) return e;
-  return launch_pdl(mla_decode_kernel<NCOL, Q8, kHide>, grid, dim3(kBlockThreads<Q8>), smem, stream,
+  return launch_pdl(mla_decode_kernel<NCOL, Q8, kSee>, grid, dim3(kBlockThreads<Q8>), smem, stream,
                     1, p);
 }
 
 template <int NCOL>
 static cudaError_t launch_decode_c(const DecodeParams& p, dim3 grid, size_t smem,
                                    cudaStream_t stream) {
-  if (!p.cache_q8) return launch_decode_n<NCOL, false, true>(p, grid, smem, stream);
-  return same_rows_seen(p, NCOL) ? launch_decode_n<NCOL, true, false>(p, grid, smem, stream)
-                                 : launch_decode_n<NCOL, true, true>(p, grid, smem, stream);
+  if (!p.cache_q8) return launch_decode_n<NCOL, false, kSeeSome>(p, grid, smem, stream);
+  switch (rows_see(p, NCOL)) {
+    case kSeeAll: return launch_decode_n<NCOL, true, kSeeAll>(p, grid, smem, stream);
+    case kSeeSame: return launch_decode_n<NCOL, true, kSeeSame>(p, grid, smem, stream);
+    default: return launch_decode_n<NCOL, true, kSeeSome>(p, grid, smem, stream);
+  }
 }
 
 cudaError_t launch_decode(const DecodeParams& p, int ncol, dim3 grid, size_t smem,

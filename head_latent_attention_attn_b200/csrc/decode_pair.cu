@@ -277,11 +277,12 @@ size_t decode_pair_smem_bytes(int r, int rope_half, int nslot) {
   return pair_layout(r, rope_half, nslot).total;
 }
 
-// kHide: some rows of a block may not see a token that others see, or (bf16 cache) a page may hold
-// more than the context: see kHideWarp.
-template <bool Q8, bool kHide>
+// kSee: what the rows of a block see. Over the bf16 cache, where a page may also hold more than the
+// context, it is always kSeeSome.
+template <bool Q8, RowsSee kSee>
 __global__ void __launch_bounds__(kThreads<Q8>, 1)
     mla_decode_pair_kernel(const __grid_constant__ DecodeParams p) {
+  constexpr bool kHide = kSee == kSeeSome;       // see kHideWarp
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = align_1024(smem_raw);
   const int r = p.r, rh = p.rope_half, lb = r / 128, rhalf = r / 2;
@@ -536,7 +537,7 @@ __global__ void __launch_bounds__(kThreads<Q8>, 1)
       // Only these tiles wait for this warp. The same code in the owners' loop costs every tile,
       // whether it runs or not (64 x 8192 tokens over the 8-bit cache 252 to 293 us instead of 239).
       // This warp's hand-overs still cost 11 % there (4 rows of 32 heads, 64 x 4096 tokens: 148 us
-      // instead of 133), so that blocks of rows which see the same tokens have an instance without.
+      // instead of 133), so that blocks of rows which see the same tokens have instances without (RowsSee).
       const RowsSeen seen(p, cg, kPairRows);
       UnitWalk w{sched[0], sched[1]};
       int jj0 = 0;                           // tiles before this piece
@@ -572,8 +573,9 @@ __global__ void __launch_bounds__(kThreads<Q8>, 1)
     if (has_work)
       dequant_pages<kQ8MaxBlocks / 2, 1>(p, cg, r0, r1, sched[0], sched[1], warp - kDqWarp0,
                                          int(rank) * lb, lb,
-                                         RowsSeen(p, cg, kPairRows).hidden_all, slots,
-                                         lay.slot_bytes, full, empty, wc);
+                                         kSee == kSeeAll ? 0
+                                                         : RowsSeen(p, cg, kPairRows).hidden_all,
+                                         slots, lay.slot_bytes, full, empty, wc);
   } else if (has_work) {
     auto rows = [&](auto role_tag) {
       constexpr int role = decltype(role_tag)::value;   // 0 owner, 1 sender, 2 receiver
@@ -1000,7 +1002,7 @@ extern "C" int mla_pair_trace_read(unsigned long long* host, int n) {
 
 int decode_pair_max_clusters(size_t smem) {
   // one CTA per SM by its shared memory, over either cache
-  if (cudaFuncSetAttribute(mla_decode_pair_kernel<false, true>,
+  if (cudaFuncSetAttribute(mla_decode_pair_kernel<false, kSeeSome>,
                            cudaFuncAttributeMaxDynamicSharedMemorySize,
                            int(smem)) != cudaSuccess) {
     cudaGetLastError();
@@ -1018,32 +1020,35 @@ int decode_pair_max_clusters(size_t smem) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   int n = 0;
-  if (cudaOccupancyMaxActiveClusters(&n, mla_decode_pair_kernel<false, true>, &cfg) != cudaSuccess) {
+  if (cudaOccupancyMaxActiveClusters(&n, mla_decode_pair_kernel<false, kSeeSome>, &cfg) != cudaSuccess) {
     cudaGetLastError();
     return 0;
   }
   return n;
 }
 
-template <bool Q8, bool kHide>
+template <bool Q8, RowsSee kSee>
 static cudaError_t launch_decode_pair_t(const DecodeParams& p, dim3 grid, size_t smem,
                                         cudaStream_t stream) {
   if (Q8) {
     static std::atomic<bool> known{false};
-    const cudaError_t e = check_launch_regs(mla_decode_pair_kernel<Q8, kHide>, kRegsLaunch, &known);
+    const cudaError_t e = check_launch_regs(mla_decode_pair_kernel<Q8, kSee>, kRegsLaunch, &known);
     if (e != cudaSuccess) return e;
   }
-  cudaError_t e = cudaFuncSetAttribute(mla_decode_pair_kernel<Q8, kHide>,
+  cudaError_t e = cudaFuncSetAttribute(mla_decode_pair_kernel<Q8, kSee>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
   if (e != cudaSuccess) return e;
-  return launch_pdl(mla_decode_pair_kernel<Q8, kHide>, grid, dim3(kThreads<Q8>), smem, stream, 2, p);
+  return launch_pdl(mla_decode_pair_kernel<Q8, kSee>, grid, dim3(kThreads<Q8>), smem, stream, 2, p);
 }
 
 cudaError_t launch_decode_pair(const DecodeParams& p, dim3 grid, size_t smem,
                                cudaStream_t stream) {
-  if (!p.cache_q8) return launch_decode_pair_t<false, true>(p, grid, smem, stream);
-  return same_rows_seen(p, kPairRows) ? launch_decode_pair_t<true, false>(p, grid, smem, stream)
-                                      : launch_decode_pair_t<true, true>(p, grid, smem, stream);
+  if (!p.cache_q8) return launch_decode_pair_t<false, kSeeSome>(p, grid, smem, stream);
+  switch (rows_see(p, kPairRows)) {
+    case kSeeAll: return launch_decode_pair_t<true, kSeeAll>(p, grid, smem, stream);
+    case kSeeSame: return launch_decode_pair_t<true, kSeeSame>(p, grid, smem, stream);
+    default: return launch_decode_pair_t<true, kSeeSome>(p, grid, smem, stream);
+  }
 }
 
 }  // namespace mla
