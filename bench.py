@@ -248,10 +248,11 @@ def _source_hash(cfg):
     other kernels)."""
     csrc = os.path.join(ROOT, "head_latent_attention_attn_b200", "csrc")
     files = ("decode_pair.cu" if uses_pair_kernel(cfg) else "decode.cu", "decode_sched.cuh",
-             "ptx.cuh")
+             "hide.cuh", "ptx.cuh")
     h = hashlib.sha256()
     for f in files:
-        h.update(open(os.path.join(csrc, f), "rb").read())
+        if os.path.exists(os.path.join(csrc, f)):
+            h.update(open(os.path.join(csrc, f), "rb").read())
     hdr = open(os.path.join(csrc, "kernels.h")).read()
     i = hdr.index("struct DecodeParams {")
     h.update(hdr[i:hdr.index("};", i)].encode())

@@ -691,8 +691,8 @@ mla_status build_decode(const mla_dims* dims, const void* q_ext, const void* cac
 // Where mla_decode_attn_q8 may put the contexts' rows in bf16 (behind them their block table), so
 // that each page is converted once and not by every block of query rows that reads it. A pass that
 // writes the rows first pays from three blocks on (off != 0). 8 x 4096 tokens on B200: three blocks
-// of the two-CTA kernel (128 heads, r 512) take 96 us in place and 86 converted first, eight 228 and
-// 180; three of the one-CTA kernel (64 heads, r 448) 66 and 62, eight 125 and 108.
+// of the two-CTA kernel (128 heads, r 512) take 67 us in place and 64 converted first, eight 147 and
+// 117; three of the one-CTA kernel (64 heads, r 448) 51 and 52, eight 81 and 80.
 struct RowsPlan {
   size_t off, table_off, bytes;
   int32_t tiles;

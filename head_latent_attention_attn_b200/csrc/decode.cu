@@ -366,8 +366,7 @@ __global__ void __launch_bounds__(kBlockThreads<Q8>, 1)
       __syncwarp();
     } else if (warp == 1) {
       // ================================ UMMA issuer for S^T ================================
-      // S^T(j) is issued once the whole page has landed. The PV products are issued by the
-      // softmax warps themselves, the moment P(j) is written.
+      // S^T(j) is issued once the whole page has landed (the PV products by a warp of their own).
       if (has_work && elect_one()) {
         const uint32_t idesc_s = make_idesc_bf16(64, NCOL, 0, 0);
         const uint64_t a0 = make_sdesc(smem_u32(slots), 16, 1024, kSw128);

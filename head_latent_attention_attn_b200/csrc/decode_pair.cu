@@ -80,7 +80,7 @@ constexpr int kDqWarp0 = kRowWarp0 + 12, kDqWarps = 8;
 template <bool Q8>
 constexpr int kThreads = 32 * (kDqWarp0 + (Q8 ? kDqWarps : 0));
 // The owners hold most; the issuers' and the senders' loops are as fast with what the block was
-// launched with (64 x 8192 tokens of 128 heads: 237 us; 257 with 56 for the issuers and 88 for the
+// launched with (64 x 8192 tokens of 128 heads: 237 us when these were chosen; 257 with 56 for the issuers and 88 for the
 // senders and receivers, 263 with 48 for the dequantising warps and 144 for the owners).
 constexpr int kRegsLaunch = 80, kRegsIssue = 80, kRegsOwner = 128, kRegsSender = 80,
               kRegsReceiver = 80, kRegsDequant = 56;
@@ -207,9 +207,9 @@ MLA_DEVICE uint2 ld_shared_v2(uint32_t saddr) {
 // Rounding adds half of the dropped byte; the byte moves are single byte permutes. That addition
 // would carry a NaN (all mantissa bits set, as the tensor core makes it) into the sign and hand the
 // partner a score of -0. So a NaN goes as +inf, of which the row's softmax makes NaN again where the
-// row sees the token: one fp32 minimum a score (256 rows of 128 heads over 4096 tokens: 372 -> 380 us,
-// 64 x 8192 tokens over the 8-bit cache 241 -> 241.5; looking for a NaN by the sum of a row's scores
-// first took 379 to 390 and 246 to 271).
+// row sees the token: one fp32 minimum a score (2 % for 256 rows of 128 heads over 4096 tokens, nothing
+// for 64 x 8192 tokens over the 8-bit cache; looking for a NaN by the sum of a row's scores first cost
+// 2 to 5 % and 2 to 12 %).
 MLA_DEVICE uint32_t f24_bits(float x) {
   return __float_as_uint(fminf(x, __uint_as_float(0x7F800000u))) + 0x80u;
 }
@@ -691,8 +691,8 @@ __global__ void __launch_bounds__(kThreads<Q8>, 1)
         // a row that sees nothing has a sum of 0; a NaN stays NaN in o and lse
         const float inv = (lt != 0.0f && !aborted) ? 1.0f / lt : 0.0f;
         const int64_t lat0 = int64_t(rank) * rhalf + 16 * qt;   // this thread's 16 of every 32
-        // A partial's rows start on 16-byte boundaries (r % 8 == 0, lat0 + c0 a multiple of 16);
-        // a padding row past q*H has nothing to write.
+        // A partial's pieces start on 32-byte boundaries (r % 128 == 0, lat0 + c0 a multiple of 16, the
+        // partials 256-byte aligned); a padding row past q*H has nothing to write.
         uint16_t* dst = whole ? p.o_latent + grow * r + lat0
                               : p.part_o + (int64_t(pslot) * kPairRows + n) * r + lat0;
         for (int c0 = 0; c0 < rhalf; c0 += 32, dst += 32) {
@@ -811,7 +811,7 @@ __global__ void __launch_bounds__(kThreads<Q8>, 1)
             }
             // O rows of an earlier tile of the piece: rescale (the first tile overwrites O)
             if (t > tb && __any_sync(0xffffffffu, alpha != 1.0f)) rescale_o(jj, alpha);
-            // weights 2^(s * scale - m) over the S buffer (its scores are in registers)
+            // weights 2^(s * scale - m)
             uint32_t pk[kHalfTok / 2];
             float sa = 0.0f, sc = 0.0f;
 #pragma unroll

@@ -4,16 +4,18 @@
 // A page's codes go from memory to the registers of the dequantising warps and from there, as
 // bf16, into the cache slot: no shared memory holds them in between, which the largest shapes
 // do not have. A warp converts 8 tokens (lane: token lane / 4, 16 of the 64 columns); its loads
-// of the next page are issued as soon as this page's codes have left the registers, and the TMA
-// producer brings pages into L2 ahead of them.
+// of the next page are issued as soon as this page's codes have left the registers. In the one-CTA
+// kernel the TMA producer brings pages into L2 ahead of them.
 //
 // What this costs is issue slots, which the softmax warps of the same SM need: some 12 cycles of
-// a scheduler for 4 codes of a warp. Against the bf16 cache the one-CTA kernel keeps its time, for
-// 0.56 to 0.61 of the bytes (16 rows over 1M tokens 127 us, 121 over bf16; 128 ragged sequences of
-// 32 heads 402 and 390; 64 rows over 1M tokens 158 and 137, over 64 x 8192 of r 512 139 and 132);
-// the two-CTA kernel takes 1.3 times (237 and 181 us). Measured and slower: 16 warps of half the
-// blocks, two pages ahead in registers, converting before the slot is free, S^T begun on half a
-// page, PV by latent chunk so that the slot's first blocks are free early.
+// a scheduler for 4 codes of a warp. So the 8-bit cache saves memory, not time. The one-CTA kernel
+// takes 1.0 to 1.2 times what it takes over the bf16 cache, for 0.54 to 0.61 of the bytes: 16 rows
+// over 1M tokens 130 us (122 over bf16), 64 rows over 1M tokens 159 (138), 128 ragged sequences of
+// 32 heads 402 from a cool start and 432 in a long run (390 and 410), 64 rows over 64 x 8192 of r
+// 512 139 (134). The two-CTA kernel takes 1.3 times: 64 x 8192 tokens of 128 heads 236 (183).
+// Measured and slower: 16 warps of half the blocks, two pages ahead in registers, converting before
+// the slot is free, S^T begun on half a page, PV by latent chunk so that the slot's first blocks are
+// free early.
 #pragma once
 
 #include "decode_sched.cuh"

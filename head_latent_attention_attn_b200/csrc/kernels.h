@@ -255,7 +255,7 @@ struct PrefillParams {
   int32_t* dev_error;
   int32_t batch, q_len, kv_len, heads, heads_per_group, dn, dr, dv, causal;
   int32_t head_block;        // heads whose keys and values are worked on together
-  int32_t split;             // CTAs (a cluster) that share the tiles of 256 query rows: 1, 2, 4, 8
+  int32_t split;             // CTAs (a cluster) that share the tiles of 256 query rows: 1 to 8
   float scale_log2;          // softmax_scale * log2(e)
 };
 // Query rows and tokens a call takes at most: tile arithmetic in 32 bits, and a unit of that many tokens

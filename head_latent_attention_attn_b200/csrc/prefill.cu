@@ -10,10 +10,10 @@
 // multiplications, 1280 cycles of an SM's tensor core, against 1024 cycles for its exponentials and
 // 80 KB of operands that the heads' other query tiles find in L2.
 //
-// Measured on B200: 1024 rows over 4096 tokens of 128 heads in 277 us from a cool start (1.09
-// PFLOP/s) and 318 us in a long run (947 TFLOP/s), where the card holds 990 W by lowering its clock
+// Measured on B200: 1024 rows over 4096 tokens of 128 heads in 281 us from a cool start (1.07
+// PFLOP/s) and 331 us in a long run (910 TFLOP/s), where the card holds 990 W by lowering its clock
 // to 1.62 GHz; a library matrix product sustains 1365 TFLOP/s there. Causal 4096 rows, 2 x 32
-// heads of 136 + 128: 300 and 322 us. A group's tile takes 3500 to 3700 cycles (scores 270 to read
+// heads of 136 + 128: 301 and 340 us. A group's tile takes 3500 to 3700 cycles (scores 270 to read
 // and find their maximum, 1400 for the weights, 1600 from the last weights to the next scores),
 // two groups' products 2560 of them. So the chain of a group's hand-overs bounds a cool card and
 // its power a warm one: taking up to half of the exponentials to the FMA units by a polynomial
