@@ -237,3 +237,32 @@ def test_prefill_of_many_short_prompts_with_garbage_behind_them():
     for _ in range(20):
         o, lse, _ = run(d, x, lens, lens)
         assert torch.equal(o, o0) and torch.equal(lse, lse0)
+
+
+@pytest.mark.parametrize("name,q", [("deepseek_v2", 2), ("hybrid", 3), ("qwen3_30b_a3b", 1), ("rows_64", 1)])
+def test_a_bad_query_row_stays_alone(name, q):
+    """A NaN in one head's query (in either latent half): that row is NaN, and the others are what they
+    are without it but for the roundings that a reference moved at other tiles brings: each side is
+    within its bound of the formula, so they are within twice that of one another."""
+    f = Filled(name, [700, 65], seed=3)
+    H, G, r, dr = SHAPES[name]
+    q_bits = f.query(q)
+    clean = list(both(f, q_bits))
+    kv = Q.rows(f.cache.cpu().numpy(), r, f.R)
+    scale = float(np.float32(f.dims.softmax_scale))
+    tol, lt = np.zeros((2, q * H, 1)), np.zeros((2, q * H))
+    for b, L in enumerate(f.lens):
+        row = kv[f.table[b, np.arange(L) // 64], np.arange(L) % 64]
+        t, rel, d = bounds_of(Q.bf16_to_f64(q_bits)[b].reshape(q * H, -1), row, row[:, :r], scale)
+        tol[b], lt[b] = t, d
+    tol, lt = cu(tol.reshape(2, q, H, 1)), cu(lt.reshape(2, q, H))
+    for col in (1, r - 1, r + f.R - 1):
+        bad = q_bits.copy()
+        bad[0, q - 1, H // 2, col] = NAN
+        row = (0, q - 1, H // 2)
+        for (o, lse), (o0, lse0) in zip(both(f, bad), clean):
+            assert bool(torch.isnan(o[row].float()).all()) and bool(torch.isnan(lse[row]))
+            o[row], lse[row] = o0[row], lse0[row]
+            e = (o.double() - o0.double()).abs() - 2 * rel * o0.double().abs()
+            assert bool((e <= 2 * tol).all())
+            assert bool(((lse - lse0).abs() <= 2 * (lt + 2.0 ** -22 * lse0.abs())).all())
