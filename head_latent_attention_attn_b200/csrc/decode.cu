@@ -640,12 +640,12 @@ __global__ void __launch_bounds__(kBlockThreads<Q8>, 1)
             }
           }
           // a token that some row does not see (the rows that see it have their NaN by its score, taken
-          // above), or past the context, where a page may hold anything
-          // (over the 8-bit cache what no row sees is zero from the conversion on). The code
-          // alone costs there (4 rows of 16 heads over 16 x 64K tokens 147 us instead of 143, 2 of 28
-          // heads over 64 x 4096 51 instead of 47), so that blocks of rows which see the same tokens
-          // have instances without it (RowsSee).
-          if (kSee == kSeeSome && ragged && pos >= L - seen_by.hidden_some && !(Q8 && pos >= L - seen_by.hidden_all)) {
+          // above), or past the context, where a page may hold anything (over the 8-bit cache what no
+          // row sees is zero from the conversion on). The code alone costs there (4 rows of 16 heads
+          // over 16 x 64K tokens 147 us instead of 143, 2 of 28 heads over 64 x 4096 51 instead of 47),
+          // so that blocks of rows which see the same tokens have instances without it (RowsSee).
+          if (kSee == kSeeSome && ragged && pos >= L - seen_by.hidden_some &&
+              !(Q8 && pos >= L - seen_by.hidden_all)) {
             (void)mbar_try_wait(&full[slot], ring.round & 1);   // long complete: the page's bytes
             uint8_t* row = slots + slot * slot_bytes + tok * 128;
             for (int k = hf; k < (p.r + 63) / 64; k += 2)

@@ -26,7 +26,8 @@
 // tile j have been read, not for PV of tile j.
 //
 // Roles (512 threads): warp 0 TMA producer, warp 1 S issuer and TMEM owner, warp 2 PV
-// issuer, warp 3 what some rows do not see, warps 4-15 the rows. TMEM lane n holds row n and a warp reaches only the 32 lanes
+// issuer, warp 3 what some rows do not see, warps 4-15 the rows. TMEM lane n holds row n and
+// a warp reaches only the 32 lanes
 // of its sub-partition (warp % 4). CTA k owns the rows on lanes 16k..16k+15 of every
 // sub-partition, so each of the three row roles has one warp on every SM sub-partition
 // (its issue slots and MUFU units). With 16x32bx2 TMEM accesses a warp covers 16 lanes,
@@ -80,8 +81,9 @@ constexpr int kDqWarp0 = kRowWarp0 + 12, kDqWarps = 8;
 template <bool Q8>
 constexpr int kThreads = 32 * (kDqWarp0 + (Q8 ? kDqWarps : 0));
 // The owners hold most; the issuers' and the senders' loops are as fast with what the block was
-// launched with (64 x 8192 tokens of 128 heads: 237 us when these were chosen; 257 with 56 for the issuers and 88 for the
-// senders and receivers, 263 with 48 for the dequantising warps and 144 for the owners).
+// launched with (64 x 8192 tokens of 128 heads: 237 us when these were chosen; 257 with 56 for the
+// issuers and 88 for the senders and receivers, 263 with 48 for the dequantising warps and 144 for
+// the owners).
 constexpr int kRegsLaunch = 80, kRegsIssue = 80, kRegsOwner = 128, kRegsSender = 80,
               kRegsReceiver = 80, kRegsDequant = 56;
 // setmaxnreg may only lower a group's share by .dec and raise it by .inc
@@ -533,11 +535,12 @@ __global__ void __launch_bounds__(kThreads<Q8>, 1)
     } else if (kHide && warp == kHideWarp && has_work) {
       // ========================== tokens that some row does not see ========================
       // Once S of a tile has been computed, such a token's latent half loses what a weight of 0 must
-      // not meet (see hide_token; the rows that see it have their NaN by its score); over the bf16 cache what lies past the context is zeroed here too.
-      // Only these tiles wait for this warp. The same code in the owners' loop costs every tile,
-      // whether it runs or not (64 x 8192 tokens over the 8-bit cache 252 to 293 us instead of 239).
-      // This warp's hand-overs still cost 11 % there (4 rows of 32 heads, 64 x 4096 tokens: 148 us
-      // instead of 133), so that blocks of rows which see the same tokens have instances without (RowsSee).
+      // not meet (see hide_token; the rows that see it have their NaN by its score); over the bf16
+      // cache what lies past the context is zeroed here too. Only these tiles wait for this warp. The
+      // same code in the owners' loop costs every tile, whether it runs or not (64 x 8192 tokens over
+      // the 8-bit cache 252 to 293 us instead of 239). This warp's hand-overs still cost 11 % there (4
+      // rows of 32 heads, 64 x 4096 tokens: 148 us instead of 133), so that blocks of rows which see
+      // the same tokens have instances without (RowsSee).
       const RowsSeen seen(p, cg, kPairRows);
       UnitWalk w{sched[0], sched[1]};
       int jj0 = 0;                           // tiles before this piece

@@ -49,7 +49,7 @@ struct UnitWalk {
   }
 };
 
-// Which tokens of a sequence a block of ROWS query rows sees: row (i, h) sees all but the last
+// Which tokens of a sequence a block of `rows` query rows sees: row (i, h) sees all but the last
 // q - 1 - i tokens, or with causal == 0 all of them.
 struct RowsSeen {
   int hidden_some, hidden_all;   // of the last tokens: not seen by every row, not seen by any row

@@ -77,8 +77,8 @@ MLA_DEVICE void prefetch_pages(const DecodeParams& p, int cg, int r1, int upto,
 // once. The last `hidden` tokens of a context, which none of the block's rows sees, become zeros.
 template <int NB, int NG>
 MLA_DEVICE void dequant_pages(const DecodeParams& p, int cg, int r0, int r1, int b, int s, int grp,
-                              int blk0, int nb, int hidden, uint8_t* slots,
-                              uint32_t slot_bytes, uint64_t* full, uint64_t* empty, const WaitCtx& wc) {
+                              int blk0, int nb, int hidden, uint8_t* slots, uint32_t slot_bytes,
+                              uint64_t* full, uint64_t* empty, const WaitCtx& wc) {
   const int lane = threadIdx.x & 31, part = lane & 3;
   const int tok = 8 * NG * grp + (lane >> 2);       // of the first group; + 8 g
   const int not_live = hidden + tok;

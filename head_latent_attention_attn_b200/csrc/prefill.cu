@@ -76,7 +76,7 @@ constexpr uint32_t kMiscOff = kRopeOff + 2 * kBlk;
 constexpr uint32_t kBars = 4 + 2 * kSlots + 10 + 6;
 constexpr uint32_t kInfoOff = kMiscOff + 16;     // [2] unit descriptions, 32 bytes each
 constexpr uint32_t kRespOff = kInfoOff + 64;     // answer of the launch control, 16 bytes
-constexpr uint32_t kBadOff = kRespOff + 16;      // [4] see mark_bad
+constexpr uint32_t kBadOff = kRespOff + 16;      // [4] see bad_unit
 constexpr uint32_t kBarOff = kBadOff + 16;
 constexpr uint32_t kSmem = kBarOff + 8 * kBars + 1024;   // + alignment slack
 static_assert(kSmem <= 232448, "shared memory of a CTA");
