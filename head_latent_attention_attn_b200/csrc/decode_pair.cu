@@ -72,6 +72,8 @@ __device__ unsigned long long g_mla_pair_trace[kPairTraceEvents * kPairTraceTile
 namespace {
 
 constexpr int kPvWarp = 2, kHideWarp = 3;
+// The hiding warp waits from a range's start for its last tile: 2^25 tiles of some 2 us at most.
+constexpr uint64_t kHideLimitNs = 300000000000ull;
 // First of the 12 row warps. Over the 8-bit cache (Q8) eight more warps follow them, which
 // dequantise this CTA's half of each page, one per 8-token group. Every role but the first four
 // warps' is an aligned group of four, so that it can take its own share of the registers there
@@ -551,7 +553,7 @@ __global__ void __launch_bounds__(kThreads<Q8>, 1)
         const int tb = max(w.s, r0), te = min(w.s + w.tiles, r1);
         for (int t = max(tb, seen.first_tile(w)); t < te; ++t) {
           const int jj = jj0 + (t - tb), slot = jj % p.nslot;
-          ok = __all_sync(0xffffffffu, mbar_wait(&hide_s[slot], (phases >> slot) & 1, wc));
+          ok = __all_sync(0xffffffffu, mbar_wait<kHideLimitNs>(&hide_s[slot], (phases >> slot) & 1, wc));
           if (!ok) break;
           phases ^= 1u << slot;
           (void)mbar_try_wait(&full[slot], (jj / p.nslot) & 1);   // long complete: the page's bytes

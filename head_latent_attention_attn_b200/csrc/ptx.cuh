@@ -110,6 +110,9 @@ struct WaitCtx {
 
 constexpr uint64_t kWaitLimitNs = 2000000000ull;  // 2 s: far above any legitimate wait
 
+// kLimit: longer for a warp that others' work keeps waiting for long. Where something is wrong their
+// limits run out first, and the abort flag ends this wait too.
+template <uint64_t kLimit = kWaitLimitNs>
 MLA_DEVICE bool mbar_wait(uint64_t* bar, uint32_t parity, const WaitCtx& w) {
   if (mbar_try_wait(bar, parity)) return true;
   uint64_t t0 = globaltimer_ns();
@@ -117,7 +120,7 @@ MLA_DEVICE bool mbar_wait(uint64_t* bar, uint32_t parity, const WaitCtx& w) {
   while (true) {
     if (mbar_try_wait(bar, parity)) return true;
     if (*w.abort_flag) return false;
-    if ((++spins & 63u) == 0 && globaltimer_ns() - t0 > kWaitLimitNs) {
+    if ((++spins & 63u) == 0 && globaltimer_ns() - t0 > kLimit) {
       *w.abort_flag = 1;
       if (w.dev_error) atomicOr(w.dev_error, MLA_DEVERR_TIMEOUT);
       return false;

@@ -105,3 +105,22 @@ def test_nothing_to_do():
     assert st == mla.MLA_OK and bool((o == 7.0).all()) and bool((lse == 7.0).all())
     assert torch.equal(f.cache, before)
     assert mla.mla_get_device_status(ws.view(torch.int32)[:1]) == mla.MLA_OK
+
+
+@pytest.mark.parametrize("name,q", [("deepseek_v2", 1), ("qwen3_30b_a3b", 4)])
+def test_a_context_of_seconds_in_one_range(name, q):
+    """One page over and over as a context of 130M tokens that one cluster works through alone, longer
+    than a wait in the kernel may take: its last tile is waited for from the start."""
+    f = Filled(name, [64], seed=9)
+    d, H, r = f.dims, f.dims.num_heads, f.dims.kv_lora_rank
+    n = 2_000_000 * 64 + 17
+    table = torch.full((1, n // 64 + 1), int(f.table[0, 0]), dtype=torch.int32, device="cuda")
+    lens = torch.tensor([n], dtype=torch.int32, device="cuda")
+    x = bf(f.query(q))
+    ws = torch.zeros(mla.mla_decode_workspace_size(d, 1, q, n, 1), dtype=torch.uint8, device="cuda")
+    for fn, cache in ((mla.mla_decode_attn_q8, f.cache), (mla.mla_decode_attn, f.bf16_cache())):
+        o = torch.zeros((1, q, H, r), dtype=torch.bfloat16, device="cuda")
+        lse = torch.zeros((1, q, H), device="cuda")
+        fn(d, x, cache, table, lens, n, ws, o, lse, num_splits=1)
+        assert mla.mla_get_device_status(ws.view(torch.int32)[:1]) == mla.MLA_OK
+        assert bool(torch.isfinite(o.float()).all()) and bool((lse > np.log(n) - 30).all())
