@@ -223,8 +223,9 @@ size_t mla_decode_workspace_size(const mla_dims* dims, int32_t batch, int32_t q_
  *   max_seq_len host-side upper bound of seq_lens, used to plan the splits
  *   o_latent    bf16 [B, q, H, r] output; lse fp32 [B, q, H] output
  *   workspace   >= mla_decode_workspace_size(...) bytes, 256-byte aligned
- * Supported: ps == 64, H*q rows split in groups of <= 64 per CTA, r <= 512,
- * D <= 640. Others return MLA_ERR_UNSUPPORTED.
+ * Supported: ps == 64, H*q rows split in groups of <= 64 per CTA (of <= 128 per two CTAs
+ * where H*q > 64, r % 128 == 0 and G*d_r is 32, 64 or 128), r <= 512, D <= 640, and D <= 576
+ * where a CTA takes more than 32 rows. Others return MLA_ERR_UNSUPPORTED.
  */
 mla_status mla_decode_attn(const mla_dims* dims, const void* q_ext, const void* cache,
                            int64_t num_pages, const int32_t* block_table,
